@@ -31,7 +31,9 @@
  * Beyond the block itself: moe_forward_prenorm (the pre-norm RMSNorm fused in
  * front), moe_forward_fp8 (block-scaled FP8 expert weights),
  * moe_experts_forward (routing supplied by the caller), moe_forward_host
- * (host buffers), the step entry points, and moe_route_noalloc.
+ * (host buffers), the step entry points, moe_route_noalloc, the token
+ * dispatch with its gradients (moe_sort_tokens .. moe_undispatch_backward)
+ * and the MXFP4 experts (moe_quantize_fp4 .. moe_swiglu_fp4).
  *
  * Conventions for every entry point
  *   - Tensors are dense, row-major, in device memory unless stated otherwise,
@@ -383,6 +385,111 @@ MOE_API int moe_device_status(const void *workspace, moe_stream_t stream);
 MOE_API int moe_route_noalloc(const moe_shape *shape, const void *x, const void *W_router,
                               const float *expert_bias, int score_fn, int norm_topk, float route_scale,
                               int32_t *topk_idx, float *topk_w, moe_stream_t stream);
+
+/* ---- Token dispatch: rows in expert order and back, with the gradients ----
+ *
+ * The (token, slot) pairs of a routing, sorted by expert (stably: inside an
+ * expert by token, then by slot), give each pair a row.  These calls take the
+ * rows apart from the block above and its workspace, for training and for
+ * callers that run the experts themselves:
+ *   sort            offsets, slot_row from topk_idx
+ *   dispatch        x_sorted[slot_row[t,j]] = x[t]
+ *   undispatch      out[t] = sum_j topk_w[t,j] y[slot_row[t,j]]
+ *   and backward    dx[t] = sum_j dx_sorted[slot_row[t,j]];
+ *                   dy[slot_row[t,j]] = topk_w[t,j] dout[t],
+ *                   dw[t,j] = sum_i dout[t,i] y[slot_row[t,j],i]
+ * A slot whose expert is -1 (a padding token, a pair dropped for capacity)
+ * has row -1: nothing is read or written for it, it adds 0, its dw is 0.
+ * Sums run in slot order in fp32 and are rounded once.  Rows behind the last
+ * expert (offsets[E] and up) are never written.
+ *
+ * Conventions as above, and: 1 <= T <= 4,194,304; 1 <= k <= 32 (k may exceed
+ * E, and a token may name an expert twice: both pairs get rows);
+ * 1 <= E <= 2048; d a multiple of 64, at most 65536.  `dtype` is the type of
+ * the row tensors (MOE_BF16 ..); weights and their gradients are fp32.  The
+ * row tensors have T * k rows.  Outputs may not overlap inputs. */
+#define MOE_BF16 0
+#define MOE_FP16 1
+#define MOE_FP32 2
+
+/* Workspace of moe_sort_tokens, moe_matmul_fp4 and moe_swiglu_fp4: 256-byte
+ * aligned; its first word is the error word that moe_device_status reads.
+ * moe_sort_tokens clears it; the products only add to it, so a caller that
+ * does not sort clears the bytes once before its first product. */
+#define MOE_DISPATCH_WORKSPACE_BYTES 256
+
+/*   topk_idx [T,k] int32: experts in [0,E), or -1 for none (anything else
+ *            counts as none and moe_device_status reports MOE_ERR_INVALID_ARG).
+ *   offsets  [E+1] int32: first row of each expert; [E] = rows in all.
+ *   slot_row [T,k] int32: row of each pair, -1 for none. */
+MOE_API int moe_sort_tokens(int32_t T, int32_t k, int32_t E, const int32_t *topk_idx, int32_t *offsets,
+                            int32_t *slot_row, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* slot_row as moe_sort_tokens writes it (a row outside [0, T*k) counts as
+ * none); rows must differ from one another. */
+MOE_API int moe_dispatch(int32_t T, int32_t k, int32_t d, int dtype, const void *x, const int32_t *slot_row,
+                         void *x_sorted, moe_stream_t stream);
+MOE_API int moe_dispatch_backward(int32_t T, int32_t k, int32_t d, int dtype, const void *dx_sorted,
+                                  const int32_t *slot_row, void *dx, moe_stream_t stream);
+MOE_API int moe_undispatch(int32_t T, int32_t k, int32_t d, int dtype, const void *y, const int32_t *slot_row,
+                           const float *topk_w, void *out, moe_stream_t stream);
+MOE_API int moe_undispatch_backward(int32_t T, int32_t k, int32_t d, int dtype, const void *dout, const void *y,
+                                    const int32_t *slot_row, const float *topk_w, void *dy, float *dw,
+                                    moe_stream_t stream);
+
+/* ---- MXFP4 experts ----
+ *
+ * OCP MX blocks of 32 consecutive elements along a row, E2M1 elements and one
+ * power-of-two scale (UE8M0: its biased exponent byte) per block:
+ *     x[g,r,c] = e2m1(code) * 2^(scale - 127),  scale 255 = NaN.
+ * Unlike the FP8 weights above, which are widened to bf16, these are
+ * multiplied as they are: activations are MXFP4 too, and the tensor cores
+ * apply the scales (kind::mxf4, fp32 accumulation).
+ *   codes  uint8 [G, rows, K/2]: two codes a byte, the even element in the low half.
+ *   scales uint8 [G, ceil(K/128), rows, 4]: the four scales of 128 elements
+ *          next to one another, those of neighbouring rows behind (K not a
+ *          multiple of 128: the last two bytes of the last word are written 0
+ *          and never used).
+ * K a multiple of 64, at most 65536; G * rows at most 134,217,728. */
+typedef struct {
+  void *codes;          /* 16-byte aligned */
+  void *scales;         /* 16-byte aligned */
+} moe_fp4_tensor;
+
+/* x [G, rows, K] of `dtype` to MXFP4.  The scale of a block is
+ * 2^(floor(log2 max|x|) - 2), at least 2^-127; elements are rounded to
+ * nearest, ties to even, and saturate at 6 * scale.  A block with a NaN or an
+ * infinity gets the NaN scale and zero codes. */
+MOE_API int moe_quantize_fp4(int32_t G, int32_t rows, int32_t K, int dtype, const void *x, const moe_fp4_tensor *q,
+                             moe_stream_t stream);
+
+/* MXFP4 to `dtype` (rounded to nearest where the type cannot hold the value;
+ * bf16 and fp32 hold every value that moe_quantize_fp4 writes for them). */
+MOE_API int moe_dequantize_fp4(int32_t G, int32_t rows, int32_t K, int dtype, const moe_fp4_tensor *q, void *x,
+                               moe_stream_t stream);
+
+/* moe_quantize_fp4 and moe_dispatch in one: x [T,d] is read and quantised
+ * once, x_sorted (G = 1, rows = T*k, K = d) gets a copy per slot. */
+MOE_API int moe_dispatch_fp4(int32_t T, int32_t k, int32_t d, int dtype, const void *x, const int32_t *slot_row,
+                             const moe_fp4_tensor *x_sorted, moe_stream_t stream);
+
+/* The experts' products of sorted rows: out[r,n] = sum_c a[r,c] W[e,n,c] for
+ * offsets[e] <= r < offsets[e+1].
+ *   a (G = 1, rows, K), W (G = E, rows = N, K); offsets [E+1] int32 on the
+ *   device, not decreasing, at most `rows` (values outside are clamped: no
+ *   access leaves the tensors); out [rows, N] of `dtype`.  Rows outside every
+ *   expert are left as they were.  N a multiple of 64, at most 65536. */
+MOE_API int moe_matmul_fp4(int32_t rows, int32_t E, int32_t N, int32_t K, const moe_fp4_tensor *a,
+                           const int32_t *offsets, const moe_fp4_tensor *W, int dtype, void *out, void *workspace,
+                           size_t workspace_bytes, moe_stream_t stream);
+
+/* The gate/up half of the SwiGLU experts in one call:
+ *   h[r,j] = SiLU(a[r] . W_gate[e,j]) * (a[r] . W_up[e,j])
+ * computed in fp32 and written as MXFP4 (G = 1, rows, K = f), ready for
+ * moe_matmul_fp4 with the down weights.  Otherwise as moe_matmul_fp4. */
+MOE_API int moe_swiglu_fp4(int32_t rows, int32_t E, int32_t f, int32_t K, const moe_fp4_tensor *a,
+                           const int32_t *offsets, const moe_fp4_tensor *W_gate, const moe_fp4_tensor *W_up,
+                           const moe_fp4_tensor *h, void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* Self-test of the bounded-wait machinery: launches one block that waits on a
  * shared-memory barrier which nothing ever completes, for at most timeout_ns

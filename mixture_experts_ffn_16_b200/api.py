@@ -35,7 +35,12 @@ EXPORTED = ["moe_version", "moe_status_string", "moe_workspace_bytes", "moe_forw
             "moe_forward_host", "moe_route", "moe_permute", "moe_expert_gate_up", "moe_expert_down",
             "moe_combine", "moe_workspace_region", "moe_device_status", "moe_debug_wait_timeout",
             "moe_route_noalloc", "moe_experts_forward", "moe_rmsnorm", "moe_forward_prenorm",
-            "moe_forward_fp8", "moe_expert_gate_up_fp8", "moe_expert_down_fp8", "moe_permute_fp8"]
+            "moe_forward_fp8", "moe_expert_gate_up_fp8", "moe_expert_down_fp8", "moe_permute_fp8",
+            "moe_sort_tokens", "moe_dispatch", "moe_dispatch_backward", "moe_undispatch", "moe_undispatch_backward",
+            "moe_quantize_fp4", "moe_dequantize_fp4", "moe_dispatch_fp4", "moe_matmul_fp4", "moe_swiglu_fp4"]
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+DISPATCH_WORKSPACE_BYTES = 256
 
 
 class MoEError(RuntimeError):
@@ -52,6 +57,11 @@ class MoeShape(ctypes.Structure):
 
 class MoeFp8Weight(ctypes.Structure):
     """moe_fp8_weight: E4M3 codes [G, rows, K] and UE8M0 block scales [G, K/32, rows]."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class MoeFp4Tensor(ctypes.Structure):
+    """moe_fp4_tensor: E2M1 codes [G, rows, K/2] and UE8M0 block scales [G, ceil(K/128), rows, 4]."""
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
@@ -113,6 +123,20 @@ def load():
     lib.moe_debug_wait_timeout.argtypes = [P, SZ, ctypes.c_uint64, P]
     lib.moe_route_noalloc.restype = I
     lib.moe_route_noalloc.argtypes = [SH, P, P, P, I, I, ctypes.c_float, P, P, P]
+    F4 = ctypes.POINTER(MoeFp4Tensor)
+    for name, args in (("sort_tokens", [I, I, I, P, P, P, P, SZ, P]),
+                       ("dispatch", [I, I, I, I, P, P, P, P]),
+                       ("dispatch_backward", [I, I, I, I, P, P, P, P]),
+                       ("undispatch", [I, I, I, I, P, P, P, P, P]),
+                       ("undispatch_backward", [I, I, I, I, P, P, P, P, P, P, P]),
+                       ("quantize_fp4", [I, I, I, I, P, F4, P]),
+                       ("dequantize_fp4", [I, I, I, I, F4, P, P]),
+                       ("dispatch_fp4", [I, I, I, I, P, P, F4, P]),
+                       ("matmul_fp4", [I, I, I, I, F4, P, F4, I, P, P, SZ, P]),
+                       ("swiglu_fp4", [I, I, I, I, F4, P, F4, F4, F4, P, SZ, P])):
+        fn = getattr(lib, "moe_" + name)
+        fn.restype = I
+        fn.argtypes = args
     _lib = lib
     return lib
 
@@ -420,6 +444,160 @@ def moe_debug_wait_timeout(workspace, timeout_ns, stream=None):
     st = load().moe_debug_wait_timeout(_p(workspace, torch.uint8, None, "workspace"), workspace.numel(),
                                        int(timeout_ns), _stream(stream))
     _check(st, "moe_debug_wait_timeout")
+
+
+# ---- Token dispatch and MXFP4 experts ----
+# Sizes come from the tensors.  An MXFP4 tensor is a (codes uint8 [G, rows, K/2],
+# scales uint8 [G, ceil(K/128), rows, 4]) pair; fp4_empty allocates one.
+
+def alloc_dispatch_workspace(device=None):
+    """The workspace of moe_sort_tokens and the MXFP4 products, its error word cleared."""
+    return torch.zeros(DISPATCH_WORKSPACE_BYTES, dtype=torch.uint8, device=device or "cuda")
+
+
+def fp4_empty(G, rows, K, device=None):
+    """An uninitialised MXFP4 tensor of G x rows x K values."""
+    u8 = dict(dtype=torch.uint8, device=device or "cuda")
+    return torch.empty((G, rows, K // 2), **u8), torch.empty((G, (K + 127) // 128, rows, 4), **u8)
+
+
+def _dims(t, n, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _dtype(t, name):
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _fp4_dims(q, name):
+    if not isinstance(q, (tuple, list)) or len(q) != 2:
+        raise TypeError(f"{name}: expected a (codes, scales) pair")
+    G, rows, half = _dims(q[0], 3, name + ".codes")
+    return G, rows, 2 * half
+
+
+def _f4(q, G, rows, K, name):
+    return ctypes.byref(MoeFp4Tensor(_p(q[0], torch.uint8, (G, rows, K // 2), name + ".codes"),
+                                     _p(q[1], torch.uint8, (G, (K + 127) // 128, rows, 4), name + ".scales")))
+
+
+def _one_device(*tensors):
+    """All tensors on the current device: the library launches there, on the stream it is given."""
+    for t in tensors:
+        if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def moe_sort_tokens(topk_idx, offsets, slot_row, workspace, stream=None):
+    """Rows of the (token, slot) pairs in expert order: offsets [E+1], slot_row [T, k] (-1: no expert)."""
+    T, k = _dims(topk_idx, 2, "topk_idx")
+    E = _dims(offsets, 1, "offsets")[0] - 1
+    i32 = torch.int32
+    args = (_p(topk_idx, i32, None, "topk_idx"), _p(offsets, i32, None, "offsets"),
+            _p(slot_row, i32, (T, k), "slot_row"), _p(workspace, torch.uint8, None, "workspace"))
+    _one_device(topk_idx, offsets, slot_row, workspace)
+    _check(load().moe_sort_tokens(T, k, E, *args, workspace.numel(), _stream(stream)), "moe_sort_tokens")
+
+
+def moe_dispatch(x, slot_row, x_sorted, stream=None):
+    """x_sorted[slot_row[t, j]] = x[t]."""
+    (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
+    dt = _dtype(x, "x")
+    args = (_p(x, None, None, "x"), _p(slot_row, torch.int32, (T, k), "slot_row"),
+            _p(x_sorted, x.dtype, (T * k, d), "x_sorted"))
+    _one_device(x, slot_row, x_sorted)
+    _check(load().moe_dispatch(T, k, d, dt, *args, _stream(stream)), "moe_dispatch")
+
+
+def moe_dispatch_backward(dx_sorted, slot_row, dx, stream=None):
+    """dx[t] = sum_j dx_sorted[slot_row[t, j]]."""
+    (T, d), k = _dims(dx, 2, "dx"), _dims(slot_row, 2, "slot_row")[1]
+    dt = _dtype(dx, "dx")
+    args = (_p(dx_sorted, dx.dtype, (T * k, d), "dx_sorted"), _p(slot_row, torch.int32, (T, k), "slot_row"),
+            _p(dx, None, None, "dx"))
+    _one_device(dx_sorted, slot_row, dx)
+    _check(load().moe_dispatch_backward(T, k, d, dt, *args, _stream(stream)), "moe_dispatch_backward")
+
+
+def moe_undispatch(y, slot_row, topk_w, out, stream=None):
+    """out[t] = sum_j topk_w[t, j] y[slot_row[t, j]]."""
+    (T, d), k = _dims(out, 2, "out"), _dims(slot_row, 2, "slot_row")[1]
+    dt = _dtype(out, "out")
+    args = (_p(y, out.dtype, (T * k, d), "y"), _p(slot_row, torch.int32, (T, k), "slot_row"),
+            _p(topk_w, torch.float32, (T, k), "topk_w"), _p(out, None, None, "out"))
+    _one_device(y, slot_row, topk_w, out)
+    _check(load().moe_undispatch(T, k, d, dt, *args, _stream(stream)), "moe_undispatch")
+
+
+def moe_undispatch_backward(dout, y, slot_row, topk_w, dy, dw, stream=None):
+    """dy[slot_row[t, j]] = topk_w[t, j] dout[t]; dw[t, j] = <dout[t], y[slot_row[t, j]]>."""
+    (T, d), k = _dims(dout, 2, "dout"), _dims(slot_row, 2, "slot_row")[1]
+    dt = _dtype(dout, "dout")
+    f32 = torch.float32
+    args = (_p(dout, None, None, "dout"), _p(y, dout.dtype, (T * k, d), "y"),
+            _p(slot_row, torch.int32, (T, k), "slot_row"), _p(topk_w, f32, (T, k), "topk_w"),
+            _p(dy, dout.dtype, (T * k, d), "dy"), _p(dw, f32, (T, k), "dw"))
+    _one_device(dout, y, slot_row, topk_w, dy, dw)
+    _check(load().moe_undispatch_backward(T, k, d, dt, *args, _stream(stream)), "moe_undispatch_backward")
+
+
+def moe_quantize_fp4(x, codes, scales, stream=None):
+    """x [G, rows, K] (bf16, fp16 or fp32) to MXFP4."""
+    G, rows, K = _dims(x, 3, "x")
+    dt = _dtype(x, "x")
+    px, q = _p(x, None, None, "x"), _f4((codes, scales), G, rows, K, "q")
+    _one_device(x, codes, scales)
+    _check(load().moe_quantize_fp4(G, rows, K, dt, px, q, _stream(stream)), "moe_quantize_fp4")
+
+
+def moe_dequantize_fp4(codes, scales, x, stream=None):
+    """MXFP4 back to x [G, rows, K] (bf16, fp16 or fp32)."""
+    G, rows, K = _dims(x, 3, "x")
+    dt = _dtype(x, "x")
+    q, px = _f4((codes, scales), G, rows, K, "q"), _p(x, None, None, "x")
+    _one_device(codes, scales, x)
+    _check(load().moe_dequantize_fp4(G, rows, K, dt, q, px, _stream(stream)), "moe_dequantize_fp4")
+
+
+def moe_dispatch_fp4(x, slot_row, x_sorted, stream=None):
+    """moe_dispatch of x's MXFP4 form: x_sorted is an MXFP4 tensor (G = 1) of T * k rows."""
+    (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
+    dt = _dtype(x, "x")
+    _fp4_dims(x_sorted, "x_sorted")
+    args = (_p(x, None, None, "x"), _p(slot_row, torch.int32, (T, k), "slot_row"),
+            _f4(x_sorted, 1, T * k, d, "x_sorted"))
+    _one_device(x, slot_row, *x_sorted)
+    _check(load().moe_dispatch_fp4(T, k, d, dt, *args, _stream(stream)), "moe_dispatch_fp4")
+
+
+def moe_matmul_fp4(a, offsets, W, out, workspace, stream=None):
+    """out[r] = a[r] W[e]^T for the rows offsets[e] <= r < offsets[e+1] of every expert e."""
+    _, rows, K = _fp4_dims(a, "a")
+    E, N, _ = _fp4_dims(W, "W")
+    _dims(out, 2, "out")
+    dt = _dtype(out, "out")
+    args = (_f4(a, 1, rows, K, "a"), _p(offsets, torch.int32, (E + 1,), "offsets"), _f4(W, E, N, K, "W"), dt,
+            _p(out, None, (rows, N), "out"), _p(workspace, torch.uint8, None, "workspace"))
+    _one_device(*a, offsets, *W, out, workspace)
+    _check(load().moe_matmul_fp4(rows, E, N, K, *args, workspace.numel(), _stream(stream)), "moe_matmul_fp4")
+
+
+def moe_swiglu_fp4(a, offsets, W_gate, W_up, h, workspace, stream=None):
+    """h[r] = SiLU(a[r] W_gate[e]^T) * (a[r] W_up[e]^T), as MXFP4 (G = 1)."""
+    _, rows, K = _fp4_dims(a, "a")
+    E, f, _ = _fp4_dims(W_gate, "W_gate")
+    _fp4_dims(W_up, "W_up")
+    _fp4_dims(h, "h")
+    args = (_f4(a, 1, rows, K, "a"), _p(offsets, torch.int32, (E + 1,), "offsets"), _f4(W_gate, E, f, K, "W_gate"),
+            _f4(W_up, E, f, K, "W_up"), _f4(h, 1, rows, f, "h"), _p(workspace, torch.uint8, None, "workspace"))
+    _one_device(*a, offsets, *W_gate, *W_up, *h, workspace)
+    _check(load().moe_swiglu_fp4(rows, E, f, K, *args, workspace.numel(), _stream(stream)), "moe_swiglu_fp4")
 
 
 def workspace_view(workspace, shape, region, dtype, dims):

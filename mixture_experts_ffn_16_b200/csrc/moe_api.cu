@@ -11,17 +11,6 @@
 
 namespace moe {
 
-namespace {
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   // looked up once per process (thread-safe static initialisation); first
   // reached from device_info, after the runtime is up
@@ -36,6 +25,12 @@ EncodeTiledFn encode_fn() {
   }();
   return fn;
 }
+
+namespace {
+
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Weight tensor [G, rows, K] bf16 -> tiles of 128 rows x 64 K, 128-byte swizzle.
 bool map_weights(CUtensorMap* m, const void* ptr, int K, int rows, int G) {

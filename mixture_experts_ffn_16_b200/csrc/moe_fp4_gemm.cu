@@ -1,0 +1,587 @@
+// moe_fp4_gemm.cu - the experts' products in MXFP4 on the 5th-generation
+// tensor cores (kind::mxf4, block scales applied by the MMA):
+//
+//   product : out[r, n] = a[r,:] . W[e(r), n, :]
+//   swiglu  : h[r, j]   = SiLU(a[r,:] . Wg[e(r), j, :]) * (a[r,:] . Wu[e(r), j, :]),
+//             written as MXFP4 (a block = 32 consecutive j)
+//
+// for rows r sorted by expert, e(r) given by offsets[E+1] on the device.
+//
+// The weights are the MMA's M side and the tokens its N side: a unit of work
+// is 2 x 128 weight rows (product: 256 consecutive output features; swiglu:
+// 128 gate rows and the 128 up rows of the same features) times a run of up
+// to nmax rows of one expert, cut evenly and rounded up to 16, so that an
+// expert with few rows costs few MMA columns and no row is padded in memory.
+//
+//   warp 0      TMA: 256 elements of K a stage (128-byte swizzled rows) of both
+//               weight tiles, their scale words and the token rows.
+//   warp 1      tensor-memory owner and MMA issuer: 4 x 64 elements a stage.
+//   warps 2-5   scales to tensor memory: the MMA reads them there, row r of a
+//               tile in lane r % 32 of column r / 32 and the same in all four
+//               lane quarters, so each of the four warps writes all of them
+//               to its quarter.  Weight scales come from the stage; token
+//               scales, whose first row may be any, straight from memory, one
+//               k-block ahead.
+//   warps 6-13  epilogue: two warps per lane quarter.  A lane is a feature and
+//               a warp's 32 lanes are one block of h: its magnitude is a warp
+//               reduction, the codes of 8 tokens and 8 features are exchanged
+//               by three shuffles.
+//
+// K need not be a multiple of 256: loads past its end read zeros, and the MMAs
+// past it are not issued.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "moe_fp4.cuh"
+#include "moe_internal.h"
+#include "moe_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kNA = 2;                                    // weight tiles per unit
+constexpr int kStageK = 256;                              // elements of K per stage
+constexpr uint32_t kTile = kTileRows * 128u;              // 128 rows x 256 codes
+constexpr uint32_t kTileScales = kTileRows * 2u * 4u;     // their scale words: 2 x 128
+constexpr int kScaleWarps = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kFirstScale = 2;
+constexpr int kFirstEpi = kFirstScale + kScaleWarps;
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kMaxBufs = 2;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kStgRow = 80;                               // 64 bytes of features + 16: distinct banks
+constexpr uint32_t kStgBytes = 16 * kStgRow;              // per epilogue warp
+constexpr int kSmemAlign = 1024;
+constexpr int kSmemTail = 512;                            // barriers, TMEM slot, abort flag
+constexpr size_t kSmemBudget = 232448;
+
+constexpr int64_t kMaxUnits = 1 << 30;
+
+enum OutKind { kOutBf16 = 0, kOutFp16 = 1, kOutFp32 = 2, kOutSwiglu = 3 };
+
+struct Params {
+  CUtensorMap mapW[kNA];     // codes: product: [0] both tiles; swiglu: gate, up
+  CUtensorMap mapWs[kNA];    // scale words
+  CUtensorMap mapA[4];       // token codes, boxes of 16 / 32 / 64 / 128 rows
+  const uint32_t* a_scales;  // [KC][rows]
+  const int32_t* offsets;
+  void* out;
+  uint8_t* out_scales;
+  uint32_t* err;
+  int rows, E, N, K;
+  int nmax, stages, nbuf, sf_base;
+  uint64_t timeout_ns;
+};
+
+struct Unit {
+  int e, wb, row0, rows, n;
+};
+
+// Columns of the scale words of one stage: per weight tile 2 chunks of 128
+// elements x 4 columns of 32 rows; the token tile 2 chunks x NB columns.
+template <int NB>
+constexpr int sf_cols() { return kNA * 8 + 2 * NB; }
+
+__device__ __forceinline__ int runs_of(int rows, int nmax) { return (rows + nmax - 1) / nmax; }
+
+// The expert that owns unit u: the last e with first[e] <= u.  The whole warp
+// searches: 32 probes spread over the experts, then 32 at a time between two.
+__device__ __forceinline__ Unit find_unit(const int* first, const int* off, int E, int nmax, int u, int lane) {
+  const int step = (E + 31) / 32;
+  const int i = lane * step;
+  const uint32_t m = __ballot_sync(0xffffffffu, i < E && first[i] <= u);
+  const int b = (__popc(m) - 1) * step;
+  int cnt = 0;
+  for (int j = 0; j < step; j += 32) {
+    const int q = b + j + lane;
+    cnt += __popc(__ballot_sync(0xffffffffu, j + lane < step && q < E && first[q] <= u));
+  }
+  Unit un;
+  un.e = b + cnt - 1;
+  const int c = off[un.e + 1] - off[un.e];
+  const int nr = runs_of(c, nmax);
+  const int per = ((c + nr - 1) / nr + 15) & ~15;
+  const int v = u - first[un.e];
+  un.wb = v / nr;
+  const int run = v - un.wb * nr;
+  un.row0 = off[un.e] + run * per;
+  un.rows = min(per, c - run * per);
+  un.n = (un.rows + 15) & ~15;
+  return un;
+}
+
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (global_timer_ns() - t0 > timeout_ns) return;
+  }
+}
+
+// One lane waits, the warp learns the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, volatile int* abort_flag,
+                                          const Params& p) {
+  int got = 1;
+  if (lane == 0) got = mbar_wait(bar, parity, abort_flag, p.err, p.timeout_ns) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
+
+template <int KIND>
+__device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi) {
+  if constexpr (KIND == kOutFp16) {
+    const __half2 v = __floats2half2_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// 8 lanes x 8 nibbles transposed: lane l of each group of 8 gives nibble t
+// for its feature and token t, and gets token l's nibbles of the 8 features.
+__device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane) {
+  uint32_t s = __shfl_xor_sync(0xffffffffu, w, 4);
+  w = (lane & 4) ? ((s >> 16) | (w & 0xFFFF0000u)) : ((w & 0x0000FFFFu) | (s << 16));
+  s = __shfl_xor_sync(0xffffffffu, w, 2);
+  w = (lane & 2) ? (((s >> 8) & 0x00FF00FFu) | (w & 0xFF00FF00u)) : ((w & 0x00FF00FFu) | ((s & 0x00FF00FFu) << 8));
+  s = __shfl_xor_sync(0xffffffffu, w, 1);
+  w = (lane & 1) ? (((s >> 4) & 0x0F0F0F0Fu) | (w & 0xF0F0F0F0u)) : ((w & 0x0F0F0F0Fu) | ((s & 0x0F0F0F0Fu) << 4));
+  return w;
+}
+
+// SiLU(g) u.  The result is rounded to 3 bits and a value next to a border
+// moves by a whole step, so the sigmoid is computed to a few fp32 ulps
+// (exponential and division of the special-function unit, not tanh.approx's
+// 2^-11).
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+template <int KIND, int NB>
+__global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
+  constexpr bool SWIGLU = KIND == kOutSwiglu;
+  constexpr int kRowsPerWb = SWIGLU ? kTileRows : kNA * kTileRows;   // weight rows between units
+  constexpr int kSf = sf_cols<NB>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
+  const int S = p.stages;
+  const uint32_t tok_off = kNA * kTile, sc_off = tok_off + static_cast<uint32_t>(p.nmax) * 128u;
+  const uint32_t stage_bytes = sc_off + kNA * kTileScales;    // a multiple of 1024: nmax is one of 8 at least
+  uint8_t* stg_all = smem + static_cast<size_t>(S) * stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * kStgBytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* sfull = empty + kMaxStages;
+  uint64_t* tfull = sfull + kMaxStages;
+  uint64_t* tempty = tfull + kMaxBufs;
+  uint64_t* drain = tempty + kMaxBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int64_t* wsum = reinterpret_cast<int64_t*>(tmem_slot + 2);   // one per warp
+  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + kSmemTail);   // [E + 1] row offsets, clamped
+  int* first = off + p.E + 1;                                  // [E + 1] first unit of each expert
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+      mbar_init(sfull + s, kScaleWarps);
+    }
+    for (int b = 0; b < kMaxBufs; ++b) {
+      mbar_init(tfull + b, 1);
+      mbar_init(tempty + b, kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    for (int i = 0; i < kNA; ++i) {
+      prefetch_tensormap(&p.mapW[i]);
+      prefetch_tensormap(&p.mapWs[i]);
+    }
+    for (int i = 0; i < 4; ++i) prefetch_tensormap(&p.mapA[i]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  chain_wait();
+
+  // Units of each expert.  Offsets are clamped to the rows there are, an
+  // expert whose end lies before its start gets none, and the count saturates
+  // (valid offsets stay below kMaxUnits), so nothing is read or written out
+  // of bounds whatever the offsets say.
+  for (int e = tid; e <= p.E; e += kThreads) off[e] = min(max(__ldg(p.offsets + e), 0), p.rows);
+  __syncthreads();
+  const int nwb = (p.N + kRowsPerWb - 1) / kRowsPerWb;
+  {
+    const int per = (p.E + kThreads - 1) / kThreads;
+    const int e0 = tid * per, e1 = min(e0 + per, p.E);
+    int64_t sum = 0;
+    for (int e = e0; e < e1; ++e) sum += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t at = inc - sum;
+    for (int w = 0; w < warp; ++w) at += wsum[w];
+    for (int e = e0; e < e1; ++e) {
+      first[e] = static_cast<int>(min(at, kMaxUnits));
+      at += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
+    }
+    // threads past the experts carry the total
+    if (tid == kThreads - 1) first[p.E] = static_cast<int>(min(at, kMaxUnits));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int num_units = first[p.E];
+  const int KB = (p.K + kStageK - 1) / kStageK;
+  const int grid = gridDim.x;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < num_units; u += grid) {
+      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const int f0 = un.wb * kRowsPerWb;
+      const int na = (!SWIGLU && f0 + kTileRows >= p.N) ? 1 : kNA;      // the second tile may lie past the weight
+      const uint32_t tx = static_cast<uint32_t>(na) * (kTile + kTileScales) + static_cast<uint32_t>(un.n) * 128u;
+      if (lane == 0) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
+          const uint32_t fb = smem_u32(&full[stage]);
+          mbar_arrive_expect_tx(&full[stage], tx);
+          for (int a = 0; a < na; ++a) {
+            const int row = f0 + (SWIGLU ? 0 : a * kTileRows);
+            tma_load_3d_hint(sbase + a * kTile, &p.mapW[SWIGLU ? a : 0], fb, kb * 128, row, un.e, pol_w);
+            tma_load_3d_hint(sbase + sc_off + a * kTileScales, &p.mapWs[SWIGLU ? a : 0], fb, row, 2 * kb, un.e,
+                             pol_w);
+          }
+          tma_load_rows<false>(sbase + tok_off, p.mapA, fb, kb * 128, un.row0, un.n, pol_a);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    }
+    if (lane == 0) {
+      // leave no copy in flight
+      const uint32_t outstanding = issued < static_cast<uint32_t>(S) ? issued : static_cast<uint32_t>(S);
+      for (uint32_t i = 1; i <= outstanding; ++i) {
+        const uint32_t I = issued - i;
+        wait_drain(&full[I % S], (I / S) & 1u, p.timeout_ns);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    int stage = 0;
+    uint32_t phase = 0, count = 0;
+    bool any = false, ok = true;
+    for (int u = blockIdx.x; ok && u < num_units; u += grid) {
+      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      if (lane == 0) {
+        const int na = (!SWIGLU && un.wb * kRowsPerWb + kTileRows >= p.N) ? 1 : kNA;
+        const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
+        const uint32_t bpar = (count / static_cast<uint32_t>(p.nbuf)) & 1u;
+        ok = mbar_wait(&tempty[buf], bpar ^ 1u, abort_flag, p.err, p.timeout_ns);
+        tc_fence_after();
+        const uint32_t id0 = idesc_mxf4(kTileRows, un.n, 0), id1 = idesc_mxf4(kTileRows, un.n, 1);
+        const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * kNA * p.nmax);
+        for (int kb = 0; ok && kb < KB; ++kb) {
+          ok = mbar_wait(&full[stage], phase, abort_flag, p.err, p.timeout_ns) &&
+               mbar_wait(&sfull[stage], phase, abort_flag, p.err, p.timeout_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
+          const uint64_t bdesc = sw128_kmajor_desc(sbase + tok_off);
+          const uint32_t sf = tmem_base + static_cast<uint32_t>(p.sf_base + stage * kSf);
+          const int steps = min(4, (p.K - kb * kStageK) / 64);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            if (ks < steps) {
+              for (int a = 0; a < na; ++a)
+                tc_mma_mxf4(dcol + static_cast<uint32_t>(a * p.nmax), sw128_kmajor_desc(sbase + a * kTile) + 2u * ks,
+                            bdesc + 2u * ks, (ks & 1) ? id1 : id0, sf + static_cast<uint32_t>(8 * a + 4 * (ks >> 1)),
+                            sf + static_cast<uint32_t>(kNA * 8 + NB * (ks >> 1)), (kb | ks) != 0 ? 1u : 0u);
+            }
+          }
+          any = true;
+          tc_commit(&empty[stage]);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc_commit(&tfull[buf]);
+        ++count;
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    }
+    if (lane == 0 && any) {
+      // leave no MMA in flight
+      tc_commit(drain);
+      wait_drain(drain, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp < kFirstEpi) {
+    // ------------------------------------------------------------ scales
+    const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const int KC = (p.K + 127) / 128;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < num_units; u += grid) {
+      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const int na = (!SWIGLU && un.wb * kRowsPerWb + kTileRows >= p.N) ? 1 : kNA;
+      // Token scales of k-block kb: word c of chunk h is that of row 32 c +
+      // lane.  Rows past the run are read too where memory has them; their
+      // columns are never stored.
+      auto load_tok = [&](uint32_t (&w)[2 * NB], int kb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t* src = p.a_scales + static_cast<size_t>(min(2 * kb + h, KC - 1)) * p.rows;
+#pragma unroll
+          for (int c = 0; c < NB; ++c)
+            w[h * NB + c] = (32 * c < un.n) ? __ldg(src + min(un.row0 + 32 * c + lane, p.rows - 1)) : 0u;
+        }
+      };
+      uint32_t tok[2 * NB], nxt[2 * NB];
+      load_tok(tok, 0);
+      for (int kb = 0; kb < KB; ++kb) {
+        if (kb + 1 < KB) load_tok(nxt, kb + 1);
+        ok = warp_wait(&full[stage], phase, lane, abort_flag, p);
+        if (!ok) break;
+        tc_fence_after();          // the stage's earlier MMAs, which read these columns, are done
+        const uint32_t* sw =
+            reinterpret_cast<const uint32_t*>(smem + static_cast<size_t>(stage) * stage_bytes + sc_off);
+        const uint32_t sf = tmem_base + quarter + static_cast<uint32_t>(p.sf_base + stage * kSf);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = (i < 8 || na == 2) ? sw[32 * i + lane] : 0u;
+        tmem_st_32x32b_x16(sf, w);
+        if constexpr (NB == 4)
+          tmem_st_32x32b_x8(sf + kNA * 8, tok);
+        else
+          tmem_st_32x32b_x16(sf + kNA * 8, tok);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[stage]);
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) tok[i] = nxt[i];
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
+    uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
+    const uint32_t stg_s = smem_u32(stg);
+    uint32_t count = 0;
+    for (int u = blockIdx.x; u < num_units; u += grid, ++count) {
+      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
+      const uint32_t bpar = (count / static_cast<uint32_t>(p.nbuf)) & 1u;
+      if (!warp_wait(&tfull[buf], bpar, lane, abort_flag, p)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                          static_cast<uint32_t>(buf * kNA * p.nmax);
+      // column blocks of 16 tokens, every second one
+      if constexpr (SWIGLU) {
+        const int feat0 = un.wb * kTileRows + 32 * q;
+        if (feat0 < p.N) {
+          uint8_t* codes = static_cast<uint8_t*>(p.out);
+          for (int c = 16 * half; c < un.n; c += 32) {
+            uint32_t g[16], v[16];
+            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), g);
+            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(p.nmax + c), v);
+            tmem_ld_wait();
+            uint32_t byte = 0;      // lane j: scale byte of token c + j
+            float h[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              h[j] = swiglu(__uint_as_float(g[j]), __uint_as_float(v[j]));
+              const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+              const uint32_t b = fp4_scale_byte(m);
+              h[j] = (b == kFp4NanScale) ? 0.0f : h[j] * fp4_inv_scale(b);
+              if (lane == j) byte = b;
+            }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              float t[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) t[j] = h[8 * o + j];
+              const uint32_t w = transpose_nibbles(e2m1x8(t), lane);
+              const int tok = c + 8 * o + (lane & 7);
+              if (tok < un.rows)
+                *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(un.row0 + tok) * (p.N / 2) + feat0 / 2 +
+                                             4 * (lane >> 3)) = w;
+            }
+            if (lane < 16 && c + lane < un.rows)
+              p.out_scales[(static_cast<size_t>(un.wb) * p.rows + un.row0 + c + lane) * 4 + q] =
+                  static_cast<uint8_t>(byte);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int a = 0; a < kNA; ++a) {
+          const int feat0 = un.wb * kRowsPerWb + a * kTileRows + 32 * q;
+          if (feat0 >= p.N) break;
+          const uint32_t ta = tb + static_cast<uint32_t>(a * p.nmax);
+          for (int c = 16 * half; c < un.n; c += 32) {
+            if constexpr (KIND == kOutFp32) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(ta + static_cast<uint32_t>(c), v);
+              tmem_ld_wait();
+              float* out = static_cast<float*>(p.out) + static_cast<size_t>(un.row0 + c) * p.N + feat0 + lane;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (c + j < un.rows) out[static_cast<size_t>(j) * p.N] = __uint_as_float(v[j]);
+            } else {
+              uint32_t v[2][8];
+              tmem_ld_16x256b_x2(ta + static_cast<uint32_t>(c), v[0]);
+              tmem_ld_16x256b_x2(ta + (16u << 16) + static_cast<uint32_t>(c), v[1]);
+              tmem_ld_wait();
+              // matrices: 0 = features 16h + 0..7 x tokens 0..7, 1 = features
+              // 16h + 8..15 x tokens 0..7, 2 and 3 = the same for tokens 8..15
+              const int mi = lane >> 3, mj = lane & 7;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                stmatrix_x4_trans(
+                    stg_s + static_cast<uint32_t>((8 * (mi >> 1) + mj) * kStgRow + (16 * h + 8 * (mi & 1)) * 2),
+                    pack16<KIND>(v[h][0], v[h][1]), pack16<KIND>(v[h][2], v[h][3]), pack16<KIND>(v[h][4], v[h][5]),
+                    pack16<KIND>(v[h][6], v[h][7]));
+              __syncwarp();
+#pragma unroll
+              for (int rep = 0; rep < 2; ++rep) {
+                const int cc = lane + 32 * rep;
+                const int tok = cc >> 2, part = cc & 3;
+                if (c + tok < un.rows)
+                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                            static_cast<size_t>(un.row0 + c + tok) * p.N + feat0 + part * 8) =
+                      *reinterpret_cast<const uint4*>(stg + tok * kStgRow + part * 16);
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[buf]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  EncodeTiledFn fn = encode_fn();
+  return fn && fn(m, type, rank, const_cast<void*>(ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Weight codes uint8 [E, N, K/2]: tiles of 128 rows x 128 bytes, swizzled.
+// Scale words [E, KC, N]: tiles of 2 x 128.
+bool map_weight(CUtensorMap* codes_map, CUtensorMap* scales_map, const void* codes, const void* scales, int E, int N,
+                int K) {
+  const cuuint64_t KC = (K + 127) / 128, n = N, half = K / 2;
+  const cuuint64_t d[3] = {half, n, static_cast<cuuint64_t>(E)}, s[2] = {half, half * n};
+  const cuuint32_t b[3] = {128, kTileRows, 1};
+  const cuuint64_t ds[3] = {n, KC, static_cast<cuuint64_t>(E)}, ss[2] = {4 * n, 4 * n * KC};
+  const cuuint32_t bs[3] = {kTileRows, 2, 1};
+  return encode(codes_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode(scales_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, scales, ds, ss, bs, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+size_t smem_bytes(int nmax, int E, int stages) {
+  const size_t stage = kNA * (kTile + kTileScales) + static_cast<size_t>(nmax) * 128;
+  return kSmemAlign + stages * stage + kEpiWarps * kStgBytes + kSmemTail + 2 * (static_cast<size_t>(E) + 1) * 4;
+}
+
+template <int KIND, int NB>
+int launch_kind(const Params& prm, int grid, size_t smem, cudaStream_t st) {
+  static std::atomic<int> limit[64];
+  const int rc = raise_smem_limit(fp4_gemm_kernel<KIND, NB>, limit, static_cast<int>(smem));
+  if (rc != MOE_OK) return rc;
+  return launch_chained(fp4_gemm_kernel<KIND, NB>, dim3(grid), dim3(kThreads), smem, st, prm) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err, cudaStream_t st) {
+  const bool swiglu = q.w1_codes != nullptr;
+  Params p;
+  // Rows per run: the smallest step that holds the average expert.
+  const int64_t avg = (static_cast<int64_t>(q.rows) + q.E - 1) / q.E;
+  p.nmax = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 96;
+  p.nbuf = 2;
+  const int sf = sf_cols<4>();
+  p.stages = kMaxStages;
+  while (p.stages > 2 && (smem_bytes(p.nmax, q.E, p.stages) > kSmemBudget ||
+                          p.nbuf * kNA * p.nmax + p.stages * sf > static_cast<int>(kTmemCols)))
+    --p.stages;
+  p.sf_base = static_cast<int>(kTmemCols) - p.stages * sf;
+  const size_t smem = smem_bytes(p.nmax, q.E, p.stages);
+  if (smem > kSmemBudget || p.nbuf * kNA * p.nmax > p.sf_base) return MOE_ERR_UNSUPPORTED;
+
+  if (!map_weight(&p.mapW[0], &p.mapWs[0], q.w0_codes, q.w0_scales, q.E, q.N, q.K)) return MOE_ERR_CUDA;
+  if (!map_weight(&p.mapW[1], &p.mapWs[1], swiglu ? q.w1_codes : q.w0_codes, swiglu ? q.w1_scales : q.w0_scales, q.E,
+                  q.N, q.K))
+    return MOE_ERR_CUDA;
+  for (int b = 0; b < 4; ++b) {
+    const cuuint64_t d[2] = {static_cast<cuuint64_t>(q.K / 2), static_cast<cuuint64_t>(q.rows)};
+    const cuuint64_t s[1] = {static_cast<cuuint64_t>(q.K / 2)};
+    const cuuint32_t box[2] = {128, 16u << b};
+    if (!encode(&p.mapA[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q.a_codes, d, s, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return MOE_ERR_CUDA;
+  }
+  p.a_scales = static_cast<const uint32_t*>(q.a_scales);
+  p.offsets = q.offsets;
+  p.out = q.out;
+  p.out_scales = static_cast<uint8_t*>(q.out_scales);
+  p.err = err;
+  p.rows = q.rows;
+  p.E = q.E;
+  p.N = q.N;
+  p.K = q.K;
+  p.timeout_ns = kWaitTimeoutNs;
+  const int grid = di.sms;
+  if (swiglu) return launch_kind<kOutSwiglu, 4>(p, grid, smem, st);
+  switch (q.dtype) {
+    case MOE_BF16: return launch_kind<kOutBf16, 4>(p, grid, smem, st);
+    case MOE_FP16: return launch_kind<kOutFp16, 4>(p, grid, smem, st);
+    default: return launch_kind<kOutFp32, 4>(p, grid, smem, st);
+  }
+}
+
+}  // namespace moe

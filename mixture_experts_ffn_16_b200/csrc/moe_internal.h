@@ -176,6 +176,42 @@ int launch_combine(const Plan& p, void* out, char* ws, const void* x, const void
 
 int launch_wait_timeout(uint32_t* err, uint64_t timeout_ns, cudaStream_t st);
 
+// Token dispatch (moe_dispatch.cu).  Rows are bytes unless a dtype (MOE_BF16 ..) is given.
+int launch_sort_tokens(int T, int k, int E, const int32_t* topk_idx, int32_t* offsets, int32_t* slot_row,
+                       uint32_t* err, cudaStream_t st);
+int launch_dispatch(int T, int k, size_t row_bytes, const void* x, const int32_t* slot_row, void* x_sorted,
+                    cudaStream_t st);
+int launch_undispatch(int T, int k, int d, int dtype, const void* y, const int32_t* slot_row, const float* topk_w,
+                      void* out, cudaStream_t st);
+int launch_undispatch_backward(int T, int k, int d, int dtype, const void* dout, const void* y,
+                               const int32_t* slot_row, const float* topk_w, void* dy, float* dw, cudaStream_t st);
+
+// MXFP4 conversion (moe_fp4_quant.cu).
+int launch_quantize_fp4(int G, int rows, int K, int dtype, const void* x, void* codes, void* scales,
+                        cudaStream_t st);
+int launch_dequantize_fp4(int G, int rows, int K, int dtype, const void* codes, const void* scales, void* x,
+                          cudaStream_t st);
+int launch_dispatch_fp4(int T, int k, int d, int dtype, const void* x, const int32_t* slot_row, void* codes,
+                        void* scales, cudaStream_t st);
+
+// MXFP4 expert products (moe_fp4_gemm.cu).  w1 == nullptr: out = a w0^T;
+// else out = MXFP4(SiLU(a w0^T) * (a w1^T)).
+struct Fp4Product {
+  int rows, E, N, K, dtype;
+  const void *a_codes, *a_scales;
+  const int32_t* offsets;
+  const void *w0_codes, *w0_scales, *w1_codes, *w1_scales;
+  void *out, *out_scales;
+};
+int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err, cudaStream_t st);
+
+// The driver's tensor-map encoder (looked up once; NULL where there is none).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
 int launch_rmsnorm(const Plan& p, const void* x, const void* gain, float eps, void* y, cudaStream_t st);
 
 }  // namespace moe

@@ -367,6 +367,34 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc
       : "memory");
 }
 
+// Instruction descriptor for kind::mxf4: E2M1 A and B (both K-major), UE8M0
+// block scales, fp32 accumulator of shape M x N.  `half` (0 or 1) says which
+// two bytes of each 32-bit scale word the instruction's two 32-blocks use
+// (scale ids 0 and 2).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+  return (static_cast<uint32_t>(2 * half) << 4)      // B scale id
+         | (1u << 7)                                 // A format: E2M1
+         | (1u << 10)                                // B format: E2M1
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (1u << 23)                                // scale format: UE8M0
+         | (static_cast<uint32_t>(M >> 4) << 24)     // M / 16
+         | (static_cast<uint32_t>(2 * half) << 29);  // A scale id
+}
+
+// D[tmem] (+)= (A . scale_A) (B . scale_B)^T over 64 E2M1 elements of K (32
+// bytes of a tile row), a scale per 32 elements.  Scales in tensor memory:
+// row r of the tile in lane r % 32 (the same in all four lane quarters) of
+// column r / 32, four scale bytes (128 elements of K) a word.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+      : "memory");
+}
+
 // Arrive once on the barrier at this shared-memory offset in every CTA of
 // `cta_mask` when all tcgen05.mma issued so far by this thread (pair form)
 // have completed.
@@ -440,6 +468,11 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
