@@ -14,15 +14,14 @@
 // expert with few rows costs few MMA columns and no row is padded in memory.
 //
 //   warp 0      TMA: 256 elements of K a stage (128-byte swizzled rows) of both
-//               weight tiles, their scale words and the token rows.
-//   warp 1      tensor-memory owner and MMA issuer: 4 x 64 elements a stage.
-//   warps 2-5   scales to tensor memory: the MMA reads them there, row r of a
-//               tile in lane r % 32 of column r / 32 and the same in all four
-//               lane quarters, so each of the four warps writes all of them
-//               to its quarter.  Weight scales come from the stage; token
-//               scales, whose first row may be any, straight from memory, one
-//               k-block ahead.
-//   warps 6-13  epilogue: two warps per lane quarter.  A lane is a feature and
+//               weight tiles and the token rows.
+//   warp 1      tensor-memory owner and MMA issuer: copies the stage's scales
+//               to tensor memory, where the MMA reads them, then 4 x 64
+//               elements of K.
+//   warp 2      scales: 4-byte asynchronous copies (the first row of a token
+//               run may be any) that land word (row 32 c + l) of 128 rows at
+//               16 l + 4 c, the order in which tc_cp_scales reads them.
+//   warps 4-11  epilogue: two warps per lane quarter.  A lane is a feature and
 //               a warp's 32 lanes are one block of h: its magnitude is a warp
 //               reduction, the codes of 8 tokens and 8 features are exchanged
 //               by three shuffles.
@@ -43,11 +42,10 @@ namespace {
 constexpr int kNA = 2;                                    // weight tiles per unit
 constexpr int kStageK = 256;                              // elements of K per stage
 constexpr uint32_t kTile = kTileRows * 128u;              // 128 rows x 256 codes
-constexpr uint32_t kTileScales = kTileRows * 2u * 4u;     // their scale words: 2 x 128
-constexpr int kScaleWarps = 4;
+constexpr uint32_t kChunkScales = kTileRows * 4u;         // scale words of 128 rows x 128 elements
 constexpr int kEpiWarps = 8;
-constexpr int kFirstScale = 2;
-constexpr int kFirstEpi = kFirstScale + kScaleWarps;
+constexpr int kEpiPer = kEpiWarps / 4;                    // epilogue warps per lane quarter
+constexpr int kFirstEpi = 4;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kMaxBufs = 2;
 constexpr int kMaxStages = 8;
@@ -64,8 +62,8 @@ enum OutKind { kOutBf16 = 0, kOutFp16 = 1, kOutFp32 = 2, kOutSwiglu = 3 };
 
 struct Params {
   CUtensorMap mapW[kNA];     // codes: product: [0] both tiles; swiglu: gate, up
-  CUtensorMap mapWs[kNA];    // scale words
   CUtensorMap mapA[4];       // token codes, boxes of 16 / 32 / 64 / 128 rows
+  const uint32_t* w_scales[kNA];   // words [E][KC][N]
   const uint32_t* a_scales;  // [KC][rows]
   const int32_t* offsets;
   void* out;
@@ -73,17 +71,18 @@ struct Params {
   uint32_t* err;
   int rows, E, N, K;
   int nmax, stages, nbuf, sf_base;
-  uint64_t timeout_ns;
+  int64_t timeout_cycles;
 };
 
 struct Unit {
   int e, wb, row0, rows, n;
 };
 
-// Columns of the scale words of one stage: per weight tile 2 chunks of 128
-// elements x 4 columns of 32 rows; the token tile 2 chunks x NB columns.
+// Scales of one stage: 2 chunks of 128 elements for each 128 rows of the
+// weight tiles, then of the token run (NB of 128 rows each); 4 columns of
+// tensor memory each.
 template <int NB>
-constexpr int sf_cols() { return kNA * 8 + 2 * NB; }
+constexpr int sf_chunks() { return 2 * (kNA + NB); }
 
 __device__ __forceinline__ int runs_of(int rows, int nmax) { return (rows + nmax - 1) / nmax; }
 
@@ -113,11 +112,35 @@ __device__ __forceinline__ Unit find_unit(const int* first, const int* off, int 
   return un;
 }
 
-__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+// Bounded wait for a barrier phase: the thread sleeps in the hardware, up to
+// 20 us an attempt.  The clock is read every 8 attempts only.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           const Params& p) {
   const uint32_t a = smem_u32(bar);
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (global_timer_ns() - t0 > timeout_ns) return;
+  if (mbar_try_wait(a, parity)) return true;
+  int64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait_sleep(a, parity, 20000u)) return true;
+    if ((it & 7u) == 0) {
+      if (*abort_flag) return false;
+      const int64_t now = clock64();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > p.timeout_cycles) {
+        *abort_flag = 1;
+        atomicOr(p.err, kDevErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+// The same for work this block itself put in flight, before it leaves: does
+// not give up for another role's sake.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, const Params& p) {
+  const uint32_t a = smem_u32(bar);
+  const int64_t t0 = clock64();
+  while (!mbar_try_wait(a, parity) && clock64() - t0 <= p.timeout_cycles) {
   }
 }
 
@@ -125,7 +148,7 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, uint6
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, volatile int* abort_flag,
                                           const Params& p) {
   int got = 1;
-  if (lane == 0) got = mbar_wait(bar, parity, abort_flag, p.err, p.timeout_ns) ? 1 : 0;
+  if (lane == 0) got = wait_phase(bar, parity, abort_flag, p) ? 1 : 0;
   return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
@@ -158,22 +181,41 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane) {
 // 2^-11).
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// The MMAs of one stage: scales to tensor memory, then `steps` x 64 elements
+// of K for each of the unit's NA weight tiles.
+template <int NA, int NB>
+__device__ __forceinline__ void issue_stage(uint32_t a_lo, uint32_t b_lo, uint64_t s_desc, uint32_t sf, uint32_t dcol,
+                                            int nmax, uint32_t id0, uint32_t id1, int kb, int steps) {
+#pragma unroll
+  for (int i = 0; i < sf_chunks<NB>(); ++i)
+    if (i < 2 * NA || i >= 2 * kNA) tc_cp_scales(sf + 4u * i, s_desc + static_cast<uint64_t>(i * (kChunkScales >> 4)));
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    if (ks < steps) {
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+        tc_mma_mxf4(dcol + static_cast<uint32_t>(a * nmax), a_lo + a * (kTile >> 4) + 2u * ks, b_lo + 2u * ks,
+                    (ks & 1) ? id1 : id0, sf + 4u * (2 * a + (ks >> 1)), sf + 4u * (2 * kNA + NB * (ks >> 1)),
+                    (kb | ks) != 0);
+    }
+  }
+}
+
 template <int KIND, int NB>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
   constexpr bool SWIGLU = KIND == kOutSwiglu;
   constexpr int kRowsPerWb = SWIGLU ? kTileRows : kNA * kTileRows;   // weight rows between units
-  constexpr int kSf = sf_cols<NB>();
+  constexpr int kSf = sf_chunks<NB>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
   const int S = p.stages;
   const uint32_t tok_off = kNA * kTile, sc_off = tok_off + static_cast<uint32_t>(p.nmax) * 128u;
-  const uint32_t stage_bytes = sc_off + kNA * kTileScales;    // a multiple of 1024: nmax is one of 8 at least
+  const uint32_t stage_bytes = sc_off + kSf * kChunkScales;   // a multiple of 1024
   uint8_t* stg_all = smem + static_cast<size_t>(S) * stage_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * kStgBytes);
   uint64_t* empty = full + kMaxStages;
-  uint64_t* sfull = empty + kMaxStages;
-  uint64_t* tfull = sfull + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + kMaxBufs;
   uint64_t* drain = tempty + kMaxBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -185,9 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full + s, 1);
+      mbar_init(full + s, 1 + 32);     // the TMA warp and the lanes of the scale warp
       mbar_init(empty + s, 1);
-      mbar_init(sfull + s, kScaleWarps);
     }
     for (int b = 0; b < kMaxBufs; ++b) {
       mbar_init(tfull + b, 1);
@@ -196,10 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    for (int i = 0; i < kNA; ++i) {
-      prefetch_tensormap(&p.mapW[i]);
-      prefetch_tensormap(&p.mapWs[i]);
-    }
+    for (int i = 0; i < kNA; ++i) prefetch_tensormap(&p.mapW[i]);
     for (int i = 0; i < 4; ++i) prefetch_tensormap(&p.mapA[i]);
   }
   if (warp == 1) {
@@ -255,22 +293,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
       const int f0 = un.wb * kRowsPerWb;
       const int na = (!SWIGLU && f0 + kTileRows >= p.N) ? 1 : kNA;      // the second tile may lie past the weight
-      const uint32_t tx = static_cast<uint32_t>(na) * (kTile + kTileScales) + static_cast<uint32_t>(un.n) * 128u;
-      if (lane == 0) {
+      const uint32_t tx = static_cast<uint32_t>(na) * kTile + static_cast<uint32_t>(un.n) * 128u;
+      if (elect_one()) {
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, p.timeout_ns)) {
+          if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p)) {
             ok = false;
             break;
           }
           const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
           const uint32_t fb = smem_u32(&full[stage]);
           mbar_arrive_expect_tx(&full[stage], tx);
-          for (int a = 0; a < na; ++a) {
-            const int row = f0 + (SWIGLU ? 0 : a * kTileRows);
-            tma_load_3d_hint(sbase + a * kTile, &p.mapW[SWIGLU ? a : 0], fb, kb * 128, row, un.e, pol_w);
-            tma_load_3d_hint(sbase + sc_off + a * kTileScales, &p.mapWs[SWIGLU ? a : 0], fb, row, 2 * kb, un.e,
-                             pol_w);
-          }
+          for (int a = 0; a < na; ++a)
+            tma_load_3d_hint(sbase + a * kTile, &p.mapW[SWIGLU ? a : 0], fb, kb * 128,
+                             f0 + (SWIGLU ? 0 : a * kTileRows), un.e, pol_w);
           tma_load_rows<false>(sbase + tok_off, p.mapA, fb, kb * 128, un.row0, un.n, pol_a);
           ++issued;
           if (++stage == S) {
@@ -279,14 +314,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
           }
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0) {
+    if (elect_one()) {
       // leave no copy in flight
       const uint32_t outstanding = issued < static_cast<uint32_t>(S) ? issued : static_cast<uint32_t>(S);
       for (uint32_t i = 1; i <= outstanding; ++i) {
         const uint32_t I = issued - i;
-        wait_drain(&full[I % S], (I / S) & 1u, p.timeout_ns);
+        wait_drain(&full[I % S], (I / S) & 1u, p);
       }
     }
   } else if (warp == 1) {
@@ -294,34 +329,30 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     int stage = 0;
     uint32_t phase = 0, count = 0;
     bool any = false, ok = true;
+    const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + tok_off);
+    const uint64_t s_lo = rows16_desc(smem_u32(smem) + sc_off);
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
       const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
-      if (lane == 0) {
+      if (elect_one()) {
         const int na = (!SWIGLU && un.wb * kRowsPerWb + kTileRows >= p.N) ? 1 : kNA;
         const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
         const uint32_t bpar = (count / static_cast<uint32_t>(p.nbuf)) & 1u;
-        ok = mbar_wait(&tempty[buf], bpar ^ 1u, abort_flag, p.err, p.timeout_ns);
+        ok = wait_phase(&tempty[buf], bpar ^ 1u, abort_flag, p);
         tc_fence_after();
         const uint32_t id0 = idesc_mxf4(kTileRows, un.n, 0), id1 = idesc_mxf4(kTileRows, un.n, 1);
         const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * kNA * p.nmax);
         for (int kb = 0; ok && kb < KB; ++kb) {
-          ok = mbar_wait(&full[stage], phase, abort_flag, p.err, p.timeout_ns) &&
-               mbar_wait(&sfull[stage], phase, abort_flag, p.err, p.timeout_ns);
+          ok = wait_phase(&full[stage], phase, abort_flag, p);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
-          const uint64_t bdesc = sw128_kmajor_desc(sbase + tok_off);
-          const uint32_t sf = tmem_base + static_cast<uint32_t>(p.sf_base + stage * kSf);
+          fence_proxy_async_smem();      // scales written by cp.async are read by the tensor core
+          const uint32_t off_s = static_cast<uint32_t>(stage) * (stage_bytes >> 4);
+          const uint32_t sf = tmem_base + static_cast<uint32_t>(p.sf_base + stage * 4 * kSf);
           const int steps = min(4, (p.K - kb * kStageK) / 64);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            if (ks < steps) {
-              for (int a = 0; a < na; ++a)
-                tc_mma_mxf4(dcol + static_cast<uint32_t>(a * p.nmax), sw128_kmajor_desc(sbase + a * kTile) + 2u * ks,
-                            bdesc + 2u * ks, (ks & 1) ? id1 : id0, sf + static_cast<uint32_t>(8 * a + 4 * (ks >> 1)),
-                            sf + static_cast<uint32_t>(kNA * 8 + NB * (ks >> 1)), (kb | ks) != 0 ? 1u : 0u);
-            }
-          }
+          if (na == kNA)
+            issue_stage<kNA, NB>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
+          else
+            issue_stage<1, NB>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
           any = true;
           tc_commit(&empty[stage]);
           if (++stage == S) {
@@ -332,69 +363,65 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         if (ok) tc_commit(&tfull[buf]);
         ++count;
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0 && any) {
+    if (elect_one() && any) {
       // leave no MMA in flight
       tc_commit(drain);
-      wait_drain(drain, 0, p.timeout_ns);
+      wait_drain(drain, 0, p);
     }
     __syncwarp();
-  } else if (warp < kFirstEpi) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------ scales
-    const uint32_t quarter = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const int KC = (p.K + 127) / 128;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
       const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
-      const int na = (!SWIGLU && un.wb * kRowsPerWb + kTileRows >= p.N) ? 1 : kNA;
-      // Token scales of k-block kb: word c of chunk h is that of row 32 c +
-      // lane.  Rows past the run are read too where memory has them; their
-      // columns are never stored.
-      auto load_tok = [&](uint32_t (&w)[2 * NB], int kb) {
+      const int f0 = un.wb * kRowsPerWb;
+      // Rows past the weight or the run repeat the last one there is; their
+      // results are never stored.
+      uint32_t wrow[kNA][4], trow[4 * NB];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int a = 0; a < kNA; ++a)
+          wrow[a][c] = static_cast<uint32_t>(min(f0 + (SWIGLU ? 0 : a * kTileRows) + 32 * c + lane, p.N - 1));
+      }
+#pragma unroll
+      for (int c = 0; c < 4 * NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
+        if (!ok) break;
+        const uint32_t dst = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes) + sc_off + 16u * lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t* src = p.a_scales + static_cast<size_t>(min(2 * kb + h, KC - 1)) * p.rows;
+          const int kc = min(2 * kb + h, KC - 1);
+          const size_t wchunk = (static_cast<size_t>(un.e) * KC + kc) * p.N;
+          const uint32_t* tsrc = p.a_scales + static_cast<size_t>(kc) * p.rows;
 #pragma unroll
-          for (int c = 0; c < NB; ++c)
-            w[h * NB + c] = (32 * c < un.n) ? __ldg(src + min(un.row0 + 32 * c + lane, p.rows - 1)) : 0u;
+          for (int a = 0; a < kNA; ++a) {
+            const uint32_t* wsrc = p.w_scales[a] + wchunk;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) cp_async_4(dst + (2 * a + h) * kChunkScales + 4 * c, wsrc + wrow[a][c]);
+          }
+#pragma unroll
+          for (int c = 0; c < 4 * NB; ++c)
+            if (32 * c < un.n)
+              cp_async_4(dst + (2 * kNA + NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
         }
-      };
-      uint32_t tok[2 * NB], nxt[2 * NB];
-      load_tok(tok, 0);
-      for (int kb = 0; kb < KB; ++kb) {
-        if (kb + 1 < KB) load_tok(nxt, kb + 1);
-        ok = warp_wait(&full[stage], phase, lane, abort_flag, p);
-        if (!ok) break;
-        tc_fence_after();          // the stage's earlier MMAs, which read these columns, are done
-        const uint32_t* sw =
-            reinterpret_cast<const uint32_t*>(smem + static_cast<size_t>(stage) * stage_bytes + sc_off);
-        const uint32_t sf = tmem_base + quarter + static_cast<uint32_t>(p.sf_base + stage * kSf);
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = (i < 8 || na == 2) ? sw[32 * i + lane] : 0u;
-        tmem_st_32x32b_x16(sf, w);
-        if constexpr (NB == 4)
-          tmem_st_32x32b_x8(sf + kNA * 8, tok);
-        else
-          tmem_st_32x32b_x16(sf + kNA * 8, tok);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[stage]);
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) tok[i] = nxt[i];
+        cp_async_mbar_arrive_noinc(&full[stage]);
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-  } else {
+    cp_async_wait_all();
+  } else if (warp >= kFirstEpi) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
+    const int q = warp & 3, part4 = (warp - kFirstEpi) >> 2;
     uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
     const uint32_t stg_s = smem_u32(stg);
     uint32_t count = 0;
@@ -406,12 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                           static_cast<uint32_t>(buf * kNA * p.nmax);
-      // column blocks of 16 tokens, every second one
+      // column blocks of 16 tokens, every kEpiPer-th one
       if constexpr (SWIGLU) {
         const int feat0 = un.wb * kTileRows + 32 * q;
         if (feat0 < p.N) {
           uint8_t* codes = static_cast<uint8_t*>(p.out);
-          for (int c = 16 * half; c < un.n; c += 32) {
+          for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer) {
             uint32_t g[16], v[16];
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), g);
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(p.nmax + c), v);
@@ -448,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
           const int feat0 = un.wb * kRowsPerWb + a * kTileRows + 32 * q;
           if (feat0 >= p.N) break;
           const uint32_t ta = tb + static_cast<uint32_t>(a * p.nmax);
-          for (int c = 16 * half; c < un.n; c += 32) {
+          for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer) {
             if constexpr (KIND == kOutFp32) {
               uint32_t v[16];
               tmem_ld_32x32b_x16(ta + static_cast<uint32_t>(c), v);
@@ -509,20 +536,15 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr,
 }
 
 // Weight codes uint8 [E, N, K/2]: tiles of 128 rows x 128 bytes, swizzled.
-// Scale words [E, KC, N]: tiles of 2 x 128.
-bool map_weight(CUtensorMap* codes_map, CUtensorMap* scales_map, const void* codes, const void* scales, int E, int N,
-                int K) {
-  const cuuint64_t KC = (K + 127) / 128, n = N, half = K / 2;
+bool map_weight(CUtensorMap* m, const void* codes, int E, int N, int K) {
+  const cuuint64_t n = N, half = K / 2;
   const cuuint64_t d[3] = {half, n, static_cast<cuuint64_t>(E)}, s[2] = {half, half * n};
   const cuuint32_t b[3] = {128, kTileRows, 1};
-  const cuuint64_t ds[3] = {n, KC, static_cast<cuuint64_t>(E)}, ss[2] = {4 * n, 4 * n * KC};
-  const cuuint32_t bs[3] = {kTileRows, 2, 1};
-  return encode(codes_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B) &&
-         encode(scales_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, scales, ds, ss, bs, CU_TENSOR_MAP_SWIZZLE_NONE);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-size_t smem_bytes(int nmax, int E, int stages) {
-  const size_t stage = kNA * (kTile + kTileScales) + static_cast<size_t>(nmax) * 128;
+size_t smem_bytes(int nmax, int chunks, int E, int stages) {
+  const size_t stage = kNA * kTile + static_cast<size_t>(nmax) * 128 + chunks * kChunkScales;
   return kSmemAlign + stages * stage + kEpiWarps * kStgBytes + kSmemTail + 2 * (static_cast<size_t>(E) + 1) * 4;
 }
 
@@ -536,6 +558,16 @@ int launch_kind(const Params& prm, int grid, size_t smem, cudaStream_t st) {
              : MOE_ERR_CUDA;
 }
 
+template <int NB>
+int launch_nb(OutKind kind, const Params& prm, int grid, size_t smem, cudaStream_t st) {
+  switch (kind) {
+    case kOutBf16: return launch_kind<kOutBf16, NB>(prm, grid, smem, st);
+    case kOutFp16: return launch_kind<kOutFp16, NB>(prm, grid, smem, st);
+    case kOutFp32: return launch_kind<kOutFp32, NB>(prm, grid, smem, st);
+    default: return launch_kind<kOutSwiglu, NB>(prm, grid, smem, st);
+  }
+}
+
 }  // namespace
 
 int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err, cudaStream_t st) {
@@ -545,19 +577,21 @@ int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err,
   const int64_t avg = (static_cast<int64_t>(q.rows) + q.E - 1) / q.E;
   p.nmax = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 96;
   p.nbuf = 2;
-  const int sf = sf_cols<4>();
+  const bool wide = p.nmax > kTileRows;
+  const int chunks = wide ? sf_chunks<2>() : sf_chunks<1>();
   p.stages = kMaxStages;
-  while (p.stages > 2 && (smem_bytes(p.nmax, q.E, p.stages) > kSmemBudget ||
-                          p.nbuf * kNA * p.nmax + p.stages * sf > static_cast<int>(kTmemCols)))
+  while (p.stages > 2 && (smem_bytes(p.nmax, chunks, q.E, p.stages) > kSmemBudget ||
+                          p.nbuf * kNA * p.nmax + p.stages * 4 * chunks > static_cast<int>(kTmemCols)))
     --p.stages;
-  p.sf_base = static_cast<int>(kTmemCols) - p.stages * sf;
-  const size_t smem = smem_bytes(p.nmax, q.E, p.stages);
+  p.sf_base = static_cast<int>(kTmemCols) - p.stages * 4 * chunks;
+  const size_t smem = smem_bytes(p.nmax, chunks, q.E, p.stages);
   if (smem > kSmemBudget || p.nbuf * kNA * p.nmax > p.sf_base) return MOE_ERR_UNSUPPORTED;
 
-  if (!map_weight(&p.mapW[0], &p.mapWs[0], q.w0_codes, q.w0_scales, q.E, q.N, q.K)) return MOE_ERR_CUDA;
-  if (!map_weight(&p.mapW[1], &p.mapWs[1], swiglu ? q.w1_codes : q.w0_codes, swiglu ? q.w1_scales : q.w0_scales, q.E,
-                  q.N, q.K))
-    return MOE_ERR_CUDA;
+  for (int a = 0; a < kNA; ++a) {
+    const bool second = swiglu && a == 1;
+    if (!map_weight(&p.mapW[a], second ? q.w1_codes : q.w0_codes, q.E, q.N, q.K)) return MOE_ERR_CUDA;
+    p.w_scales[a] = static_cast<const uint32_t*>(second ? q.w1_scales : q.w0_scales);
+  }
   for (int b = 0; b < 4; ++b) {
     const cuuint64_t d[2] = {static_cast<cuuint64_t>(q.K / 2), static_cast<cuuint64_t>(q.rows)};
     const cuuint64_t s[1] = {static_cast<cuuint64_t>(q.K / 2)};
@@ -574,14 +608,10 @@ int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err,
   p.E = q.E;
   p.N = q.N;
   p.K = q.K;
-  p.timeout_ns = kWaitTimeoutNs;
+  p.timeout_cycles = 2 * static_cast<int64_t>(kWaitTimeoutNs);   // at up to 2 GHz: 2 s or more
   const int grid = di.sms;
-  if (swiglu) return launch_kind<kOutSwiglu, 4>(p, grid, smem, st);
-  switch (q.dtype) {
-    case MOE_BF16: return launch_kind<kOutBf16, 4>(p, grid, smem, st);
-    case MOE_FP16: return launch_kind<kOutFp16, 4>(p, grid, smem, st);
-    default: return launch_kind<kOutFp32, 4>(p, grid, smem, st);
-  }
+  const OutKind kind = swiglu ? kOutSwiglu : static_cast<OutKind>(q.dtype);
+  return wide ? launch_nb<2>(kind, p, grid, smem, st) : launch_nb<1>(kind, p, grid, smem, st);
 }
 
 }  // namespace moe

@@ -30,6 +30,17 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   return t;
 }
 
+// True in one lane of a converged warp, the same one at every call.  Inside a
+// branch on it the assembler knows that a single thread is active, and tensor
+// loads, MMAs and commits, whose operands are uniform registers, are issued
+// straight; in a branch on `lane == 0` each is wrapped in a loop over the
+// active lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -210,6 +221,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint6
                : "memory");
 }
 
+// 4-byte global -> shared copy.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Arrive on `bar` once every cp.async issued so far by this thread has
 // completed; counts as one of the barrier's expected arrivals.
 __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t* bar) {
@@ -381,18 +397,44 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
          | (static_cast<uint32_t>(2 * half) << 29);  // A scale id
 }
 
+// The descriptor of sw128_kmajor_desc in two halves: the high one is a
+// constant, the low one advances with the address (16-byte units).
+constexpr uint32_t kSw128DescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+
 // D[tmem] (+)= (A . scale_A) (B . scale_B)^T over 64 E2M1 elements of K (32
-// bytes of a tile row), a scale per 32 elements.  Scales in tensor memory:
-// row r of the tile in lane r % 32 (the same in all four lane quarters) of
-// column r / 32, four scale bytes (128 elements of K) a word.
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+// bytes of a tile row), a scale per 32 elements; A and B given by the low
+// words of their descriptors.  Scales in tensor memory: row r of the tile in
+// lane r % 32 (the same in all four lane quarters) of column r / 32, four
+// scale bytes (128 elements of K) a word.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                            uint32_t sa_tmem, uint32_t sb_tmem, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa_tmem), "r"(sb_tmem)
+      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(sa_tmem),
+        "r"(sb_tmem), "n"(kSw128DescHi)
       : "memory");
+}
+
+// Shared-memory descriptor of 32 rows of 16 bytes without a swizzle, 8-row
+// groups of 128 contiguous bytes (the source of tc_cp_scales).
+__device__ __forceinline__ uint64_t rows16_desc(uint32_t saddr) {
+  uint64_t desc = 0;
+  desc |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);          // start address  [0,14)
+  desc |= static_cast<uint64_t>(128 >> 4) << 16;                    // leading byte offset [16,30)
+  desc |= static_cast<uint64_t>(128 >> 4) << 32;                    // stride byte offset [32,46)
+  desc |= static_cast<uint64_t>(1) << 46;                           // version [46,48)
+  return desc;
+}
+
+// 32 rows of 16 bytes from shared memory to 4 columns of tensor memory: row l
+// to lane l, the same in all four lane quarters (the layout of tc_mma_mxf4's
+// scales, 128 rows at a time).  Runs in order before later MMAs of the thread.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Arrive once on the barrier at this shared-memory offset in every CTA of
@@ -468,11 +510,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
