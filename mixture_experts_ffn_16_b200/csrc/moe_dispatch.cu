@@ -26,6 +26,7 @@ constexpr int kSortWarps = 16;
 constexpr int kSortThreads = 32 * kSortWarps;
 constexpr int kSortMaxCluster = 8;                       // the portable cluster size
 constexpr int kSortPer = kMaxE / kSortThreads;           // experts per thread
+constexpr int kSortBatch = 8;                            // groups of 32 slots a warp has in flight
 
 __device__ __forceinline__ uint32_t cluster_nctas() {
   uint32_t r;
@@ -64,9 +65,20 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   const int64_t lo = static_cast<int64_t>(rank * kSortWarps + warp) * run;
   const int begin = static_cast<int>(min(lo, static_cast<int64_t>(n)));
   const int end = static_cast<int>(min(lo + run, static_cast<int64_t>(n)));
-  for (int i = begin + lane; i < end; i += 32) {
-    const int e = __ldg(topk_idx + i);
-    if (e >= 0 && e < E) atomicAdd(mine + e, 1);
+  // The loads of a batch are issued before any is used.
+  auto load = [&](int (&e)[kSortBatch], int i0) {
+#pragma unroll
+    for (int q = 0; q < kSortBatch; ++q) {
+      const int i = i0 + 32 * q + lane;
+      e[q] = (i < end) ? __ldg(topk_idx + i) : -1;
+    }
+  };
+  for (int i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+    int e[kSortBatch];
+    load(e, i0);
+#pragma unroll
+    for (int q = 0; q < kSortBatch; ++q)
+      if (e[q] >= 0 && e[q] < E) atomicAdd(mine + e[q], 1);
   }
   __syncthreads();
   for (int e = tid; e < E; e += kSortThreads) {
@@ -90,8 +102,9 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
     below[q] = all[q] = 0;
     const int e = tid * per + q;
     if (q < per && e < E) {
-      for (uint32_t c = 0; c < ctas; ++c) {
-        const int v = ld_cluster(mapa_shared(smem_u32(total + e), c));
+#pragma unroll
+      for (uint32_t c = 0; c < kSortMaxCluster; ++c) {
+        const int v = c < ctas ? ld_cluster(mapa_shared(smem_u32(total + e), c)) : 0;
         if (c < rank) below[q] += v;
         all[q] += v;
       }
@@ -123,19 +136,24 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   uint32_t lt;
   asm volatile("mov.u32 %0, %%lanemask_lt;" : "=r"(lt));
   bool bad = false;
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    int e = (i < end) ? __ldg(topk_idx + i) : -1;
-    bad |= e < -1 || e >= E;
-    if (e < 0 || e >= E) e = -1;
-    const uint32_t peers = __match_any_sync(0xffffffffu, e);
-    const int rank_in = __popc(peers & lt);
-    int row = -1;
-    if (e >= 0) row = total[e] + mine[e] + rank_in;
-    __syncwarp();
-    if (e >= 0 && rank_in == 0) mine[e] += __popc(peers);
-    __syncwarp();
-    if (i < end) slot_row[i] = row;
+  for (int i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
+    int e[kSortBatch];
+    load(e, i0);
+#pragma unroll
+    for (int q = 0; q < kSortBatch; ++q) {
+      if (i0 + 32 * q >= end) break;
+      bad |= e[q] < -1 || e[q] >= E;
+      const int x = (e[q] < 0 || e[q] >= E) ? -1 : e[q];
+      const uint32_t peers = __match_any_sync(0xffffffffu, x);
+      const int rank_in = __popc(peers & lt);
+      int row = -1;
+      if (x >= 0) row = total[x] + mine[x] + rank_in;
+      __syncwarp();
+      if (x >= 0 && rank_in == 0) mine[x] += __popc(peers);
+      __syncwarp();
+      const int i = i0 + 32 * q + lane;
+      if (i < end) slot_row[i] = row;
+    }
   }
   if (bad) atomicOr(err, kDevErrBadRouting);
 }
@@ -285,7 +303,7 @@ undispatch_kernel(const uint4* __restrict__ y, const int32_t* __restrict__ slot_
 // y is read (dot product) and its row of dy written.  KM: an upper bound of k
 // that keeps the k partial dots in registers.
 template <typename T, int KM>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, KM <= 8 ? 3 : 1)
 undispatch_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict__ y,
                            const int32_t* __restrict__ slot_row, const float* __restrict__ w, uint4* __restrict__ dy,
                            float* __restrict__ dw, int tokens, int k, int units) {
