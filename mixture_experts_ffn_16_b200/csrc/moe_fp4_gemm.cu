@@ -18,9 +18,11 @@
 //   warp 1      tensor-memory owner and MMA issuer: copies the stage's scales
 //               to tensor memory, where the MMA reads them, then 4 x 64
 //               elements of K.
-//   warp 2      scales: 4-byte asynchronous copies (the first row of a token
-//               run may be any) that land word (row 32 c + l) of 128 rows at
-//               16 l + 4 c, the order in which tc_cp_scales reads them.
+//   warps 2, 3  scales, one chunk of 128 elements of K each: 4-byte
+//               asynchronous copies (the first row of a token run may be any)
+//               that land word (row 32 c + l) of 128 rows at 16 l + 4 c, the
+//               order in which tc_cp_scales reads them.  One warp for both
+//               chunks took 640-720 cycles a stage, more than the MMAs.
 //   warps 4-11  epilogue: two warps per lane quarter.  A lane is a feature and
 //               a warp's 32 lanes are one block of h: its magnitude is a warp
 //               reduction, the codes of 8 tokens and 8 features are exchanged
@@ -46,12 +48,14 @@ constexpr uint32_t kChunkScales = kTileRows * 4u;         // scale words of 128 
 constexpr int kEpiWarps = 8;
 constexpr int kEpiPer = kEpiWarps / 4;                    // epilogue warps per lane quarter
 constexpr int kFirstEpi = 4;
+constexpr int kScaleLanes = 64;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kMaxBufs = 2;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStgRow = 80;                               // 64 bytes of features + 16: distinct banks
 constexpr uint32_t kStgBytes = 16 * kStgRow;              // per epilogue warp
+constexpr uint32_t kPairStgBytes = 16384;                 // pairs: the same, or the gate/up exchange
 constexpr int kSmemAlign = 1024;
 constexpr int kSmemTail = 512;                            // barriers, TMEM slot, abort flag
 constexpr size_t kSmemBudget = 232448;
@@ -81,13 +85,45 @@ struct Unit {
 // Scales of one stage: 2 chunks of 128 elements for each 128 rows of the
 // weight tiles, then of the token run (NB of 128 rows each); 4 columns of
 // tensor memory each.
-template <int NB>
-constexpr int sf_chunks() { return 2 * (kNA + NB); }
+__host__ __device__ constexpr int sf_chunks(int na, int nb) { return 2 * (na + nb); }
 
 __device__ __forceinline__ int runs_of(int rows, int nmax) { return (rows + nmax - 1) / nmax; }
 
+// Units of each expert: first[e] = number of units before expert e's (nwb
+// weight blocks times its runs), first[E] their number.  Offsets are clamped
+// to the rows there are, an expert whose end lies before its start gets none,
+// and the count saturates (valid offsets stay below kMaxUnits), so nothing is
+// read or written out of bounds whatever the offsets say.  All threads; a
+// barrier must follow.
+__device__ __forceinline__ void unit_table(const Params& p, int nwb, int* off, int* first, int64_t* wsum) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
+  for (int e = tid; e <= p.E; e += threads) off[e] = min(max(__ldg(p.offsets + e), 0), p.rows);
+  __syncthreads();
+  const int per = (p.E + threads - 1) / threads;
+  const int e0 = tid * per, e1 = min(e0 + per, p.E);
+  int64_t sum = 0;
+  for (int e = e0; e < e1; ++e) sum += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  int64_t at = inc - sum;
+  for (int w = 0; w < warp; ++w) at += wsum[w];
+  for (int e = e0; e < e1; ++e) {
+    first[e] = static_cast<int>(min(at, kMaxUnits));
+    at += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
+  }
+  // threads past the experts carry the total
+  if (tid == threads - 1) first[p.E] = static_cast<int>(min(at, kMaxUnits));
+}
+
 // The expert that owns unit u: the last e with first[e] <= u.  The whole warp
 // searches: 32 probes spread over the experts, then 32 at a time between two.
+template <int STEP>
 __device__ __forceinline__ Unit find_unit(const int* first, const int* off, int E, int nmax, int u, int lane) {
   const int step = (E + 31) / 32;
   const int i = lane * step;
@@ -102,13 +138,13 @@ __device__ __forceinline__ Unit find_unit(const int* first, const int* off, int 
   un.e = b + cnt - 1;
   const int c = off[un.e + 1] - off[un.e];
   const int nr = runs_of(c, nmax);
-  const int per = ((c + nr - 1) / nr + 15) & ~15;
+  const int per = ((c + nr - 1) / nr + STEP - 1) & ~(STEP - 1);
   const int v = u - first[un.e];
   un.wb = v / nr;
   const int run = v - un.wb * nr;
   un.row0 = off[un.e] + run * per;
   un.rows = min(per, c - run * per);
-  un.n = (un.rows + 15) & ~15;
+  un.n = (un.rows + STEP - 1) & ~(STEP - 1);
   return un;
 }
 
@@ -181,22 +217,89 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane) {
 // 2^-11).
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// h = SiLU(g) u of this lane's feature (feat0 + lane) for 8 tokens, as MXFP4:
+// the warp's 32 features are a block.  Stores the codes and scales of rows
+// un.row0 + c .. + 7 that belong to the run.
+__device__ __forceinline__ void emit_h8(const Params& p, const Unit& un, int feat0, int c, const float (&g)[8],
+                                        const float (&u)[8], int lane) {
+  uint32_t byte = 0;      // lane j: scale byte of token c + j
+  float h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[j] = swiglu(g[j], u[j]);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+    const uint32_t b = fp4_scale_byte(m);
+    h[j] = (b == kFp4NanScale) ? 0.0f : h[j] * fp4_inv_scale(b);
+    if (lane == j) byte = b;
+  }
+  const uint32_t w = transpose_nibbles(e2m1x8(h), lane);
+  const int tok = c + (lane & 7);
+  if (tok < un.rows)
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + static_cast<size_t>(un.row0 + tok) * (p.N / 2) +
+                                 feat0 / 2 + 4 * (lane >> 3)) = w;
+  if (lane < 8 && c + lane < un.rows)
+    p.out_scales[(static_cast<size_t>(feat0 >> 7) * p.rows + un.row0 + c + lane) * 4 + ((feat0 >> 5) & 3)] =
+        static_cast<uint8_t>(byte);
+}
+
+// 16 tokens (c ..) of the accumulator at `taddr` (this warp's lane quarter,
+// features feat0 .. + 31) to the output.
+template <int KIND>
+__device__ __forceinline__ void emit_out16(const Params& p, const Unit& un, int feat0, int c, uint32_t taddr,
+                                           uint8_t* stg, int lane) {
+  if constexpr (KIND == kOutFp32) {
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(taddr, v);
+    tmem_ld_wait();
+    float* out = static_cast<float*>(p.out) + static_cast<size_t>(un.row0 + c) * p.N + feat0 + lane;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (c + j < un.rows) out[static_cast<size_t>(j) * p.N] = __uint_as_float(v[j]);
+  } else {
+    uint32_t v[2][8];
+    tmem_ld_16x256b_x2(taddr, v[0]);
+    tmem_ld_16x256b_x2(taddr + (16u << 16), v[1]);
+    tmem_ld_wait();
+    // matrices: 0 = features 16h + 0..7 x tokens 0..7, 1 = features
+    // 16h + 8..15 x tokens 0..7, 2 and 3 = the same for tokens 8..15
+    const uint32_t stg_s = smem_u32(stg);
+    const int mi = lane >> 3, mj = lane & 7;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      stmatrix_x4_trans(stg_s + static_cast<uint32_t>((8 * (mi >> 1) + mj) * kStgRow + (16 * h + 8 * (mi & 1)) * 2),
+                        pack16<KIND>(v[h][0], v[h][1]), pack16<KIND>(v[h][2], v[h][3]),
+                        pack16<KIND>(v[h][4], v[h][5]), pack16<KIND>(v[h][6], v[h][7]));
+    __syncwarp();
+#pragma unroll
+    for (int rep = 0; rep < 2; ++rep) {
+      const int cc = lane + 32 * rep;
+      const int tok = cc >> 2, part = cc & 3;
+      if (c + tok < un.rows)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(un.row0 + c + tok) * p.N +
+                                  feat0 + part * 8) = *reinterpret_cast<const uint4*>(stg + tok * kStgRow + part * 16);
+    }
+    __syncwarp();
+  }
+}
+
 // The MMAs of one stage: scales to tensor memory, then `steps` x 64 elements
-// of K for each of the unit's NA weight tiles.
-template <int NA, int NB>
+// of K for each of the unit's NA weight tiles (MAX_NA: those a stage has room
+// for).
+template <int NA, int MAX_NA, int NB, bool PAIR>
 __device__ __forceinline__ void issue_stage(uint32_t a_lo, uint32_t b_lo, uint64_t s_desc, uint32_t sf, uint32_t dcol,
                                             int nmax, uint32_t id0, uint32_t id1, int kb, int steps) {
 #pragma unroll
-  for (int i = 0; i < sf_chunks<NB>(); ++i)
-    if (i < 2 * NA || i >= 2 * kNA) tc_cp_scales(sf + 4u * i, s_desc + static_cast<uint64_t>(i * (kChunkScales >> 4)));
+  for (int i = 0; i < sf_chunks(MAX_NA, NB); ++i)
+    if (i < 2 * NA || i >= 2 * MAX_NA)
+      tc_cp_scales<PAIR>(sf + 4u * i, s_desc + static_cast<uint64_t>(i * (kChunkScales >> 4)));
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
     if (ks < steps) {
 #pragma unroll
       for (int a = 0; a < NA; ++a)
-        tc_mma_mxf4(dcol + static_cast<uint32_t>(a * nmax), a_lo + a * (kTile >> 4) + 2u * ks, b_lo + 2u * ks,
-                    (ks & 1) ? id1 : id0, sf + 4u * (2 * a + (ks >> 1)), sf + 4u * (2 * kNA + NB * (ks >> 1)),
-                    (kb | ks) != 0);
+        tc_mma_mxf4<PAIR>(dcol + static_cast<uint32_t>(a * nmax), a_lo + a * (kTile >> 4) + 2u * ks, b_lo + 2u * ks,
+                          (ks & 1) ? id1 : id0, sf + 4u * (2 * a + (ks >> 1)),
+                          sf + 4u * (2 * MAX_NA + NB * (ks >> 1)), (kb | ks) != 0);
     }
   }
 }
@@ -205,7 +308,7 @@ template <int KIND, int NB>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
   constexpr bool SWIGLU = KIND == kOutSwiglu;
   constexpr int kRowsPerWb = SWIGLU ? kTileRows : kNA * kTileRows;   // weight rows between units
-  constexpr int kSf = sf_chunks<NB>();
+  constexpr int kSf = sf_chunks(kNA, NB);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
@@ -227,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full + s, 1 + 32);     // the TMA warp and the lanes of the scale warp
+      mbar_init(full + s, 1 + kScaleLanes);     // the TMA warp and the lanes of the scale warps
       mbar_init(empty + s, 1);
     }
     for (int b = 0; b < kMaxBufs; ++b) {
@@ -246,35 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   }
   chain_wait();
 
-  // Units of each expert.  Offsets are clamped to the rows there are, an
-  // expert whose end lies before its start gets none, and the count saturates
-  // (valid offsets stay below kMaxUnits), so nothing is read or written out
-  // of bounds whatever the offsets say.
-  for (int e = tid; e <= p.E; e += kThreads) off[e] = min(max(__ldg(p.offsets + e), 0), p.rows);
-  __syncthreads();
-  const int nwb = (p.N + kRowsPerWb - 1) / kRowsPerWb;
-  {
-    const int per = (p.E + kThreads - 1) / kThreads;
-    const int e0 = tid * per, e1 = min(e0 + per, p.E);
-    int64_t sum = 0;
-    for (int e = e0; e < e1; ++e) sum += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
-    int64_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int64_t at = inc - sum;
-    for (int w = 0; w < warp; ++w) at += wsum[w];
-    for (int e = e0; e < e1; ++e) {
-      first[e] = static_cast<int>(min(at, kMaxUnits));
-      at += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
-    }
-    // threads past the experts carry the total
-    if (tid == kThreads - 1) first[p.E] = static_cast<int>(min(at, kMaxUnits));
-  }
+  unit_table(p, (p.N + kRowsPerWb - 1) / kRowsPerWb, off, first, wsum);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -290,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
-      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
       const int f0 = un.wb * kRowsPerWb;
       const int na = (!SWIGLU && f0 + kTileRows >= p.N) ? 1 : kNA;      // the second tile may lie past the weight
       const uint32_t tx = static_cast<uint32_t>(na) * kTile + static_cast<uint32_t>(un.n) * 128u;
@@ -332,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + tok_off);
     const uint64_t s_lo = rows16_desc(smem_u32(smem) + sc_off);
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
-      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
       if (elect_one()) {
         const int na = (!SWIGLU && un.wb * kRowsPerWb + kTileRows >= p.N) ? 1 : kNA;
         const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
@@ -350,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
           const uint32_t sf = tmem_base + static_cast<uint32_t>(p.sf_base + stage * 4 * kSf);
           const int steps = min(4, (p.K - kb * kStageK) / 64);
           if (na == kNA)
-            issue_stage<kNA, NB>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
+            issue_stage<kNA, kNA, NB, false>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
           else
-            issue_stage<1, NB>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
+            issue_stage<1, kNA, NB, false>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
           any = true;
           tc_commit(&empty[stage]);
           if (++stage == S) {
@@ -371,14 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       wait_drain(drain, 0, p);
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp < kFirstEpi) {
     // ------------------------------------------------------------ scales
-    const int KC = (p.K + 127) / 128;
+    const int KC = (p.K + 127) / 128, h = warp - 2;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
-      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
       const int f0 = un.wb * kRowsPerWb;
       // Rows past the weight or the run repeat the last one there is; their
       // results are never stored.
@@ -395,22 +470,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
         if (!ok) break;
         const uint32_t dst = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes) + sc_off + 16u * lane;
+        const int kc = min(2 * kb + h, KC - 1);
+        const size_t wchunk = (static_cast<size_t>(un.e) * KC + kc) * p.N;
+        const uint32_t* tsrc = p.a_scales + static_cast<size_t>(kc) * p.rows;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kc = min(2 * kb + h, KC - 1);
-          const size_t wchunk = (static_cast<size_t>(un.e) * KC + kc) * p.N;
-          const uint32_t* tsrc = p.a_scales + static_cast<size_t>(kc) * p.rows;
+        for (int a = 0; a < kNA; ++a) {
+          const uint32_t* wsrc = p.w_scales[a] + wchunk;
 #pragma unroll
-          for (int a = 0; a < kNA; ++a) {
-            const uint32_t* wsrc = p.w_scales[a] + wchunk;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) cp_async_4(dst + (2 * a + h) * kChunkScales + 4 * c, wsrc + wrow[a][c]);
-          }
-#pragma unroll
-          for (int c = 0; c < 4 * NB; ++c)
-            if (32 * c < un.n)
-              cp_async_4(dst + (2 * kNA + NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
+          for (int c = 0; c < 4; ++c) cp_async_4(dst + (2 * a + h) * kChunkScales + 4 * c, wsrc + wrow[a][c]);
         }
+#pragma unroll
+        for (int c = 0; c < 4 * NB; ++c)
+          if (32 * c < un.n)
+            cp_async_4(dst + (2 * kNA + NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
         cp_async_mbar_arrive_noinc(&full[stage]);
         if (++stage == S) {
           stage = 0;
@@ -423,10 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, part4 = (warp - kFirstEpi) >> 2;
     uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
-    const uint32_t stg_s = smem_u32(stg);
     uint32_t count = 0;
     for (int u = blockIdx.x; u < num_units; u += grid, ++count) {
-      const Unit un = find_unit(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
       const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
       const uint32_t bpar = (count / static_cast<uint32_t>(p.nbuf)) & 1u;
       if (!warp_wait(&tfull[buf], bpar, lane, abort_flag, p)) break;
@@ -437,36 +508,21 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       if constexpr (SWIGLU) {
         const int feat0 = un.wb * kTileRows + 32 * q;
         if (feat0 < p.N) {
-          uint8_t* codes = static_cast<uint8_t*>(p.out);
           for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer) {
             uint32_t g[16], v[16];
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), g);
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(p.nmax + c), v);
             tmem_ld_wait();
-            uint32_t byte = 0;      // lane j: scale byte of token c + j
-            float h[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              h[j] = swiglu(__uint_as_float(g[j]), __uint_as_float(v[j]));
-              const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-              const uint32_t b = fp4_scale_byte(m);
-              h[j] = (b == kFp4NanScale) ? 0.0f : h[j] * fp4_inv_scale(b);
-              if (lane == j) byte = b;
-            }
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
-              float t[8];
+              float gate[8], up[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) t[j] = h[8 * o + j];
-              const uint32_t w = transpose_nibbles(e2m1x8(t), lane);
-              const int tok = c + 8 * o + (lane & 7);
-              if (tok < un.rows)
-                *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(un.row0 + tok) * (p.N / 2) + feat0 / 2 +
-                                             4 * (lane >> 3)) = w;
+              for (int j = 0; j < 8; ++j) {
+                gate[j] = __uint_as_float(g[8 * o + j]);
+                up[j] = __uint_as_float(v[8 * o + j]);
+              }
+              emit_h8(p, un, feat0, c + 8 * o, gate, up, lane);
             }
-            if (lane < 16 && c + lane < un.rows)
-              p.out_scales[(static_cast<size_t>(un.wb) * p.rows + un.row0 + c + lane) * 4 + q] =
-                  static_cast<uint8_t>(byte);
           }
         }
       } else {
@@ -474,43 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         for (int a = 0; a < kNA; ++a) {
           const int feat0 = un.wb * kRowsPerWb + a * kTileRows + 32 * q;
           if (feat0 >= p.N) break;
-          const uint32_t ta = tb + static_cast<uint32_t>(a * p.nmax);
-          for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer) {
-            if constexpr (KIND == kOutFp32) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(ta + static_cast<uint32_t>(c), v);
-              tmem_ld_wait();
-              float* out = static_cast<float*>(p.out) + static_cast<size_t>(un.row0 + c) * p.N + feat0 + lane;
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c + j < un.rows) out[static_cast<size_t>(j) * p.N] = __uint_as_float(v[j]);
-            } else {
-              uint32_t v[2][8];
-              tmem_ld_16x256b_x2(ta + static_cast<uint32_t>(c), v[0]);
-              tmem_ld_16x256b_x2(ta + (16u << 16) + static_cast<uint32_t>(c), v[1]);
-              tmem_ld_wait();
-              // matrices: 0 = features 16h + 0..7 x tokens 0..7, 1 = features
-              // 16h + 8..15 x tokens 0..7, 2 and 3 = the same for tokens 8..15
-              const int mi = lane >> 3, mj = lane & 7;
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                stmatrix_x4_trans(
-                    stg_s + static_cast<uint32_t>((8 * (mi >> 1) + mj) * kStgRow + (16 * h + 8 * (mi & 1)) * 2),
-                    pack16<KIND>(v[h][0], v[h][1]), pack16<KIND>(v[h][2], v[h][3]), pack16<KIND>(v[h][4], v[h][5]),
-                    pack16<KIND>(v[h][6], v[h][7]));
-              __syncwarp();
-#pragma unroll
-              for (int rep = 0; rep < 2; ++rep) {
-                const int cc = lane + 32 * rep;
-                const int tok = cc >> 2, part = cc & 3;
-                if (c + tok < un.rows)
-                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                            static_cast<size_t>(un.row0 + c + tok) * p.N + feat0 + part * 8) =
-                      *reinterpret_cast<const uint4*>(stg + tok * kStgRow + part * 16);
-              }
-              __syncwarp();
-            }
-          }
+          for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer)
+            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(a * p.nmax + c), stg, lane);
         }
       }
       tc_fence_before();
@@ -527,6 +548,314 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   }
 }
 
+// The form for large experts, on CTA pairs (cta_group::2): 256 weight rows, 128
+// per CTA, times runs of up to 192 tokens, of which each CTA loads half; two
+// accumulators of 192 columns, so the epilogue overlaps the next unit.  Per
+// multiply-add it moves 2/3 of the bytes of the single CTA's 256 x 96 units
+// into shared memory, and half the MMAs are issued.
+//   product: CTA r has output features 128 r .. of the unit's 256.
+//   swiglu:  CTA r has features 64 r .. of the unit's 128, their gate rows in
+//            lanes 0..63 and their up rows in lanes 64..127.  A gate warp and
+//            the up warp of the same features exchange half of their values
+//            through shared memory, then each finishes 8 of 16 tokens.
+// Roles as above, in both CTAs; the MMAs are issued by the leader (rank 0)
+// for both.  cp.async can only arrive on a barrier of its own CTA, so the
+// peer's scale copies complete a barrier there, and the peer's warp 1, which
+// has no MMAs to issue, reports it to the leader's.  (A scale warp that waited
+// for its own copies and reported them itself took 1.35 us a stage: its
+// cluster-scope release waits for the copies of later stages too.)
+constexpr int kPairN = 192;
+constexpr int kPairStep = 32;                             // runs are multiples of this: half per CTA
+constexpr uint32_t kXchBytes = 2 * 2 * 32 * 8 * 4;        // per warp pair: 2 buffers x 2 directions x 32 lanes x 8 floats
+
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp4_gemm_pair_kernel(const __grid_constant__ Params p) {
+  constexpr bool SWIGLU = KIND == kOutSwiglu;
+  constexpr int kCtaFeats = SWIGLU ? kTileRows / 2 : kTileRows;      // output features per CTA
+  constexpr int kRowsPerWb = 2 * kCtaFeats;
+  constexpr int NB = 2;
+  constexpr int kSf = sf_chunks(1, NB);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
+  const int S = p.stages;
+  const uint32_t tok_off = kTile, sc_off = tok_off + static_cast<uint32_t>(p.nmax / 2) * 128u;
+  const uint32_t stage_bytes = sc_off + kSf * kChunkScales;          // a multiple of 1024
+  uint8_t* stg_all = smem + static_cast<size_t>(S) * stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kPairStgBytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
+  uint64_t* tempty = tfull + kMaxBufs;
+  uint64_t* drain = tempty + kMaxBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int64_t* wsum = reinterpret_cast<int64_t*>(tmem_slot + 2);
+  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + kSmemTail);
+  int* first = off + p.E + 1;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      // leader: TMA warps of both CTAs, its scale lanes, the peer's report;
+      // peer: its scale lanes
+      mbar_init(full + s, rank == 0 ? 2 + kScaleLanes + 1 : kScaleLanes);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < kMaxBufs; ++b) {
+      mbar_init(tfull + b, 1);
+      mbar_init(tempty + b, 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    for (int i = 0; i < kNA; ++i) prefetch_tensormap(&p.mapW[i]);
+    for (int i = 0; i < 4; ++i) prefetch_tensormap(&p.mapA[i]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  chain_wait();
+  unit_table(p, (p.N + kRowsPerWb - 1) / kRowsPerWb, off, first, wsum);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                        // the peer's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int num_units = first[p.E];
+  const int KB = (p.K + kStageK - 1) / kStageK;
+  const uint32_t full_leader = mapa_shared(smem_u32(full), 0);       // + 8 * stage
+  const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);   // + 8 * buffer
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < num_units; u += npairs) {
+      const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+      const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
+      const int half = un.n >> 1, row0 = un.row0 + static_cast<int>(rank) * half;
+      const uint32_t tx = kTile + static_cast<uint32_t>(half) * 128u;
+      if (elect_one()) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
+          const uint32_t fb = full_leader + 8u * stage;
+          mbar_arrive_expect_tx_cluster(fb, tx);
+          tma_load_3d_pair_hint(sbase, &p.mapW[0], fb, kb * 128, f0, un.e, pol_w);
+          if (SWIGLU) tma_load_3d_pair_hint(sbase + kTile / 2, &p.mapW[1], fb, kb * 128, f0, un.e, pol_w);
+          tma_load_rows<true>(sbase + tok_off, p.mapA, fb, kb * 128, row0, half, pol_a);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (rank == 0 && elect_one()) {
+      // leave no copy in flight: the leader's barriers count both CTAs'
+      const uint32_t outstanding = issued < static_cast<uint32_t>(S) ? issued : static_cast<uint32_t>(S);
+      for (uint32_t i = 1; i <= outstanding; ++i) {
+        const uint32_t I = issued - i;
+        wait_drain(&full[I % S], (I / S) & 1u, p);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (leader)
+    if (rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0, count = 0;
+      bool any = false, ok = true;
+      const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + tok_off);
+      const uint64_t s_lo = rows16_desc(smem_u32(smem) + sc_off);
+      for (int u = pair; ok && u < num_units; u += npairs) {
+        const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+        if (elect_one()) {
+          const int buf = static_cast<int>(count % kMaxBufs);
+          const uint32_t bpar = (count / kMaxBufs) & 1u;
+          ok = wait_phase(&tempty[buf], bpar ^ 1u, abort_flag, p);
+          tc_fence_after();
+          const uint32_t id0 = idesc_mxf4(2 * kTileRows, un.n, 0), id1 = idesc_mxf4(2 * kTileRows, un.n, 1);
+          const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * p.nmax);
+          for (int kb = 0; ok && kb < KB; ++kb) {
+            ok = wait_phase(&full[stage], phase, abort_flag, p);
+            if (!ok) break;
+            tc_fence_after();
+            fence_proxy_async_smem();
+            const uint32_t off_s = static_cast<uint32_t>(stage) * (stage_bytes >> 4);
+            issue_stage<1, 1, NB, true>(a_lo + off_s, b_lo + off_s, s_lo + off_s,
+                                        tmem_base + static_cast<uint32_t>(p.sf_base + stage * 4 * kSf), dcol, p.nmax,
+                                        id0, id1, kb, min(4, (p.K - kb * kStageK) / 64));
+            any = true;
+            tc_commit_pair(&empty[stage], 0x3);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) tc_commit_pair(&tfull[buf], 0x3);
+          ++count;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (elect_one() && any) {
+        // leave no MMA in flight
+        tc_commit_pair(drain, 0x1);
+        wait_drain(drain, 0, p);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- report of the peer's scales
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < num_units; u += npairs) {
+        if (elect_one()) {
+          for (int kb = 0; kb < KB; ++kb) {
+            ok = wait_phase(&full[stage], phase, abort_flag, p);
+            if (!ok) break;
+            fence_proxy_async_smem();
+            mbar_arrive_cluster(full_leader + 8u * stage);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+  } else if (warp < kFirstEpi) {
+    // ------------------------------------------------------------ scales
+    const int KC = (p.K + 127) / 128, h = warp - 2;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < num_units; u += npairs) {
+      const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+      const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
+      // Rows past the weight or the run repeat the last one there is; their
+      // results are never stored.
+      const uint32_t* wsrc[4];
+      uint32_t trow[4 * NB];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int r = SWIGLU ? f0 + 32 * (c & 1) + lane : f0 + 32 * c + lane;
+        wsrc[c] = p.w_scales[SWIGLU ? c >> 1 : 0] + static_cast<size_t>(un.e) * KC * p.N + min(r, p.N - 1);
+      }
+#pragma unroll
+      for (int c = 0; c < 4 * NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
+        if (!ok) break;
+        const uint32_t dst = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes) + sc_off + 16u * lane;
+        const int kc = min(2 * kb + h, KC - 1);
+        const uint32_t* tsrc = p.a_scales + static_cast<size_t>(kc) * p.rows;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cp_async_4(dst + h * kChunkScales + 4 * c, wsrc[c] + static_cast<size_t>(kc) * p.N);
+#pragma unroll
+        for (int c = 0; c < 4 * NB; ++c)
+          if (32 * c < un.n) cp_async_4(dst + (2 + NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
+        cp_async_mbar_arrive_noinc(&full[stage]);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    cp_async_wait_all();
+  } else if (warp >= kFirstEpi) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, part2 = (warp - kFirstEpi) >> 2;
+    uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
+    // swiglu: lane quarters q and q ^ 2 hold gate and up of the same features
+    const int wp = 2 * part2 + (q & 1);
+    float4* xch = reinterpret_cast<float4*>(stg_all + wp * kXchBytes);
+    volatile int* vote = reinterpret_cast<volatile int*>(wsum + kThreads / 32) + 2 * wp;
+    uint32_t count = 0;
+    int turn = 0;
+    for (int u = pair; u < num_units; u += npairs, ++count) {
+      const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+      const int buf = static_cast<int>(count % kMaxBufs);
+      const uint32_t bpar = (count / kMaxBufs) & 1u;
+      bool got_acc = warp_wait(&tfull[buf], bpar, lane, abort_flag, p);
+      if constexpr (SWIGLU) {
+        // Both warps of an exchange go on, or neither does: they meet at its
+        // barriers.  The slots of a unit are written again two units later.
+        volatile int* v = vote + 8 * (count & 1);
+        if (lane == 0) v[q >> 1] = got_acc;
+        named_barrier(1 + wp, 64);
+        got_acc = got_acc && v[1 - (q >> 1)] != 0;
+      }
+      if (!got_acc) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * p.nmax);
+      const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
+      const int feat0 = f0 + 32 * (SWIGLU ? q & 1 : q);
+      if (feat0 < p.N) {
+        for (int c = 16 * part2; c < un.n; c += 16 * kEpiPer) {
+          if constexpr (SWIGLU) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v);
+            tmem_ld_wait();
+            // the gate warp gives away tokens 8..15 and the up warp 0..7
+            const bool up = q >= 2;
+            float4* give = xch + (2 * turn + (up ? 1 : 0)) * 64;
+            const float4* take = xch + (2 * turn + (up ? 0 : 1)) * 64;
+            float keep[8], got[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) keep[j] = __uint_as_float(up ? v[8 + j] : v[j]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              give[32 * j + lane] =
+                  up ? make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                   __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]))
+                     : make_float4(__uint_as_float(v[8 + 4 * j]), __uint_as_float(v[9 + 4 * j]),
+                                   __uint_as_float(v[10 + 4 * j]), __uint_as_float(v[11 + 4 * j]));
+            named_barrier(1 + wp, 64);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 f = take[32 * j + lane];
+              got[4 * j] = f.x;
+              got[4 * j + 1] = f.y;
+              got[4 * j + 2] = f.z;
+              got[4 * j + 3] = f.w;
+            }
+            turn ^= 1;                   // the other buffer next: one barrier a block suffices
+            if (up)
+              emit_h8(p, un, feat0, c + 8, got, keep, lane);
+            else
+              emit_h8(p, un, feat0, c, keep, got, lane);
+          } else {
+            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(c), stg, lane);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty_leader + 8u * buf);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                        // no CTA leaves while its peer may still touch it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
 bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   const cuuint32_t one[3] = {1, 1, 1};
@@ -535,21 +864,16 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ptr,
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Weight codes uint8 [E, N, K/2]: tiles of 128 rows x 128 bytes, swizzled.
-bool map_weight(CUtensorMap* m, const void* codes, int E, int N, int K) {
+// Weight codes uint8 [E, N, K/2]: tiles of `rows` x 128 bytes, swizzled.
+bool map_weight(CUtensorMap* m, const void* codes, int E, int N, int K, int rows) {
   const cuuint64_t n = N, half = K / 2;
   const cuuint64_t d[3] = {half, n, static_cast<cuuint64_t>(E)}, s[2] = {half, half * n};
-  const cuuint32_t b[3] = {128, kTileRows, 1};
+  const cuuint32_t b[3] = {128, static_cast<cuuint32_t>(rows), 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-size_t smem_bytes(int nmax, int chunks, int E, int stages) {
-  const size_t stage = kNA * kTile + static_cast<size_t>(nmax) * 128 + chunks * kChunkScales;
-  return kSmemAlign + stages * stage + kEpiWarps * kStgBytes + kSmemTail + 2 * (static_cast<size_t>(E) + 1) * 4;
-}
-
 template <int KIND, int NB>
-int launch_kind(const Params& prm, int grid, size_t smem, cudaStream_t st) {
+int launch_single(const Params& prm, int grid, size_t smem, cudaStream_t st) {
   static std::atomic<int> limit[64];
   const int rc = raise_smem_limit(fp4_gemm_kernel<KIND, NB>, limit, static_cast<int>(smem));
   if (rc != MOE_OK) return rc;
@@ -558,14 +882,20 @@ int launch_kind(const Params& prm, int grid, size_t smem, cudaStream_t st) {
              : MOE_ERR_CUDA;
 }
 
-template <int NB>
-int launch_nb(OutKind kind, const Params& prm, int grid, size_t smem, cudaStream_t st) {
-  switch (kind) {
-    case kOutBf16: return launch_kind<kOutBf16, NB>(prm, grid, smem, st);
-    case kOutFp16: return launch_kind<kOutFp16, NB>(prm, grid, smem, st);
-    case kOutFp32: return launch_kind<kOutFp32, NB>(prm, grid, smem, st);
-    default: return launch_kind<kOutSwiglu, NB>(prm, grid, smem, st);
-  }
+template <int KIND>
+int launch_pair(const Params& prm, int grid, size_t smem, cudaStream_t st) {
+  static std::atomic<int> limit[64];
+  const int rc = raise_smem_limit(fp4_gemm_pair_kernel<KIND>, limit, static_cast<int>(smem));
+  if (rc != MOE_OK) return rc;
+  return launch_chained(fp4_gemm_pair_kernel<KIND>, dim3(grid & ~1), dim3(kThreads), smem, st, prm) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+template <int KIND>
+int launch_kind(const Params& prm, bool pair, bool wide, int grid, size_t smem, cudaStream_t st) {
+  if (pair) return launch_pair<KIND>(prm, grid, smem, st);
+  return wide ? launch_single<KIND, 2>(prm, grid, smem, st) : launch_single<KIND, 1>(prm, grid, smem, st);
 }
 
 }  // namespace
@@ -575,21 +905,28 @@ int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err,
   Params p;
   // Rows per run: the smallest step that holds the average expert.
   const int64_t avg = (static_cast<int64_t>(q.rows) + q.E - 1) / q.E;
-  p.nmax = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 96;
+  bool pair = avg > 64 && di.sms >= 2;
+  p.nmax = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : pair ? kPairN : 96;
   p.nbuf = 2;
   const bool wide = p.nmax > kTileRows;
-  const int chunks = wide ? sf_chunks<2>() : sf_chunks<1>();
-  p.stages = kMaxStages;
-  while (p.stages > 2 && (smem_bytes(p.nmax, chunks, q.E, p.stages) > kSmemBudget ||
-                          p.nbuf * kNA * p.nmax + p.stages * 4 * chunks > static_cast<int>(kTmemCols)))
-    --p.stages;
+  // Stages: what shared memory and (accumulators first) tensor memory hold.
+  const int na = pair ? 1 : kNA, chunks = sf_chunks(na, wide ? 2 : 1);
+  const size_t fixed = kSmemAlign + (pair ? kPairStgBytes : kEpiWarps * kStgBytes) + kSmemTail +
+                       2 * (static_cast<size_t>(q.E) + 1) * 4;
+  const size_t stage = na * kTile + static_cast<size_t>(pair ? p.nmax / 2 : p.nmax) * 128 + chunks * kChunkScales;
+  const int acc = p.nbuf * na * p.nmax;
+  p.stages = static_cast<int>((kSmemBudget - fixed) / stage);
+  p.stages = p.stages < kMaxStages ? p.stages : kMaxStages;
+  const int sf_stages = (static_cast<int>(kTmemCols) - acc) / (4 * chunks);
+  p.stages = p.stages < sf_stages ? p.stages : sf_stages;
+  if (p.stages < 2) return MOE_ERR_UNSUPPORTED;
   p.sf_base = static_cast<int>(kTmemCols) - p.stages * 4 * chunks;
-  const size_t smem = smem_bytes(p.nmax, chunks, q.E, p.stages);
-  if (smem > kSmemBudget || p.nbuf * kNA * p.nmax > p.sf_base) return MOE_ERR_UNSUPPORTED;
+  const size_t smem = fixed + p.stages * stage;
 
+  const int wrows = pair && swiglu ? kTileRows / 2 : kTileRows;
   for (int a = 0; a < kNA; ++a) {
     const bool second = swiglu && a == 1;
-    if (!map_weight(&p.mapW[a], second ? q.w1_codes : q.w0_codes, q.E, q.N, q.K)) return MOE_ERR_CUDA;
+    if (!map_weight(&p.mapW[a], second ? q.w1_codes : q.w0_codes, q.E, q.N, q.K, wrows)) return MOE_ERR_CUDA;
     p.w_scales[a] = static_cast<const uint32_t*>(second ? q.w1_scales : q.w0_scales);
   }
   for (int b = 0; b < 4; ++b) {
@@ -610,8 +947,12 @@ int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err,
   p.K = q.K;
   p.timeout_cycles = 2 * static_cast<int64_t>(kWaitTimeoutNs);   // at up to 2 GHz: 2 s or more
   const int grid = di.sms;
-  const OutKind kind = swiglu ? kOutSwiglu : static_cast<OutKind>(q.dtype);
-  return wide ? launch_nb<2>(kind, p, grid, smem, st) : launch_nb<1>(kind, p, grid, smem, st);
+  if (swiglu) return launch_kind<kOutSwiglu>(p, pair, wide, grid, smem, st);
+  switch (q.dtype) {
+    case MOE_BF16: return launch_kind<kOutBf16>(p, pair, wide, grid, smem, st);
+    case MOE_FP16: return launch_kind<kOutFp16>(p, pair, wide, grid, smem, st);
+    default: return launch_kind<kOutFp32>(p, pair, wide, grid, smem, st);
+  }
 }
 
 }  // namespace moe

@@ -78,6 +78,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same acquiring what threads of the whole cluster released on the
+// (local) barrier.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_try_wait, but the thread may be suspended (not spinning) for up to
 // `hint_ns` nanoseconds while the phase is still pending.
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
@@ -274,6 +288,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same publishing data that this thread (or, after a __syncwarp, its warp)
+// wrote: release semantics at cluster scope.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Arms a barrier that may live in the peer CTA with `bytes` of tensor loads
 // and arrives on it.  Relaxed: the arriving thread publishes no data of its
 // own (the bytes are counted by the loads' completion), and a cluster-scope
@@ -407,16 +427,29 @@ __device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr) { return ((sad
 // words of their descriptors.  Scales in tensor memory: row r of the tile in
 // lane r % 32 (the same in all four lane quarters) of column r / 32, four
 // scale bytes (128 elements of K) a word.
+// PAIR: M = 256 over a CTA pair as in tc_mma_bf16_pair; each CTA's tensor memory
+// holds the scales of its own 128 rows of A and of all N rows of B.
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                             uint32_t sa_tmem, uint32_t sb_tmem, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%5], [%6], p;\n\t}"
-      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(sa_tmem),
-        "r"(sb_tmem), "n"(kSw128DescHi)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%5], [%6], p;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(sa_tmem),
+          "r"(sb_tmem), "n"(kSw128DescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%5], [%6], p;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(sa_tmem),
+          "r"(sb_tmem), "n"(kSw128DescHi)
+        : "memory");
 }
 
 // Shared-memory descriptor of 32 rows of 16 bytes without a swizzle, 8-row
@@ -433,8 +466,13 @@ __device__ __forceinline__ uint64_t rows16_desc(uint32_t saddr) {
 // 32 rows of 16 bytes from shared memory to 4 columns of tensor memory: row l
 // to lane l, the same in all four lane quarters (the layout of tc_mma_mxf4's
 // scales, 128 rows at a time).  Runs in order before later MMAs of the thread.
+// PAIR: in both CTAs, each from its own shared memory.
+template <bool PAIR>
 __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Arrive once on the barrier at this shared-memory offset in every CTA of
@@ -513,6 +551,11 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Barrier `id` (1..15) of the block's hardware barriers for `threads` threads.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ---------------------------------------------------------------- chained launch
