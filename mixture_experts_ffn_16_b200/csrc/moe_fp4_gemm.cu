@@ -23,7 +23,7 @@
 //               that land word (row 32 c + l) of 128 rows at 16 l + 4 c, the
 //               order in which tc_cp_scales reads them.  One warp for both
 //               chunks took 640-720 cycles a stage, more than the MMAs.
-//   warps 4-11  epilogue: two warps per lane quarter.  A lane is a feature and
+//   warps 4-19  epilogue: four warps per lane quarter.  A lane is a feature and
 //               a warp's 32 lanes are one block of h: its magnitude is a warp
 //               reduction, the codes of 8 tokens and 8 features are exchanged
 //               by three shuffles.
@@ -50,15 +50,12 @@ constexpr int kEpiPer = kEpiWarps / 4;                    // epilogue warps per 
 constexpr int kFirstEpi = 4;
 constexpr int kScaleLanes = 64;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
-constexpr int kMaxBufs = 2;
-constexpr int kMaxStages = 8;
+constexpr int kBufs = 2;                                  // accumulators
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStgRow = 80;                               // 64 bytes of features + 16: distinct banks
 constexpr uint32_t kStgBytes = 16 * kStgRow;              // per epilogue warp
-constexpr uint32_t kPairStgBytes = 16384;                 // pairs: the same, or the gate/up exchange
 constexpr int kSmemAlign = 1024;
 constexpr int kSmemTail = 512;                            // barriers, TMEM slot, abort flag
-constexpr size_t kSmemBudget = 232448;
 
 constexpr int64_t kMaxUnits = 1 << 30;
 
@@ -74,7 +71,6 @@ struct Params {
   uint8_t* out_scales;
   uint32_t* err;
   int rows, E, N, K;
-  int nmax, stages, nbuf, sf_base;
   int64_t timeout_cycles;
 };
 
@@ -82,12 +78,29 @@ struct Unit {
   int e, wb, row0, rows, n;
 };
 
-// Scales of one stage: 2 chunks of 128 elements for each 128 rows of the
-// weight tiles, then of the token run (NB of 128 rows each); 4 columns of
-// tensor memory each.
-__host__ __device__ constexpr int sf_chunks(int na, int nb) { return 2 * (na + nb); }
+// Layout of a kernel: NA weight tiles of 128 rows and TOK token rows a stage,
+// S stages, runs of up to NMAX tokens in multiples of STEP.
+template <int NA_, int NMAX_, int TOK_, int STEP_, int S_, uint32_t STG_>
+struct Form {
+  static constexpr int NA = NA_, NMAX = NMAX_, STEP = STEP_, S = S_;
+  static constexpr int NB = (NMAX + kTileRows - 1) / kTileRows;    // 128s of tokens
+  // Scales of one stage: 2 chunks of 128 elements for each 128 rows of the
+  // weight tiles, then of the run; 4 columns of tensor memory each.
+  static constexpr int kChunks = 2 * (NA + NB);
+  static constexpr uint32_t kTokOff = NA * kTile, kScaleOff = kTokOff + TOK_ * 128u;
+  static constexpr uint32_t kStage = kScaleOff + kChunks * kChunkScales;
+  static constexpr uint32_t kStg = STG_;                             // epilogue staging
+  static constexpr uint32_t kSfBase = kTmemCols - S * 4 * kChunks;   // its columns behind the accumulators
+  static constexpr uint32_t kFixed = kSmemAlign + S * kStage + kStg + kSmemTail;
+  static_assert(kStage % 1024 == 0 && kTokOff % 1024 == 0, "swizzled tiles start at multiples of 1024");
+  static_assert(kBufs * NA * NMAX <= static_cast<int>(kSfBase), "tensor memory");
+  static_assert(kFixed + 2 * 4 * (kMaxE + 1) <= 232448, "shared memory, with the tables of kMaxE experts");
+};
 
-__device__ __forceinline__ int runs_of(int rows, int nmax) { return (rows + nmax - 1) / nmax; }
+template <class F>
+__device__ __forceinline__ int runs_of(int rows) {
+  return (rows + F::NMAX - 1) / F::NMAX;
+}
 
 // Units of each expert: first[e] = number of units before expert e's (nwb
 // weight blocks times its runs), first[E] their number.  Offsets are clamped
@@ -95,6 +108,7 @@ __device__ __forceinline__ int runs_of(int rows, int nmax) { return (rows + nmax
 // and the count saturates (valid offsets stay below kMaxUnits), so nothing is
 // read or written out of bounds whatever the offsets say.  All threads; a
 // barrier must follow.
+template <class F>
 __device__ __forceinline__ void unit_table(const Params& p, int nwb, int* off, int* first, int64_t* wsum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
   for (int e = tid; e <= p.E; e += threads) off[e] = min(max(__ldg(p.offsets + e), 0), p.rows);
@@ -102,7 +116,7 @@ __device__ __forceinline__ void unit_table(const Params& p, int nwb, int* off, i
   const int per = (p.E + threads - 1) / threads;
   const int e0 = tid * per, e1 = min(e0 + per, p.E);
   int64_t sum = 0;
-  for (int e = e0; e < e1; ++e) sum += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
+  for (int e = e0; e < e1; ++e) sum += static_cast<int64_t>(runs_of<F>(max(off[e + 1] - off[e], 0))) * nwb;
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -115,7 +129,7 @@ __device__ __forceinline__ void unit_table(const Params& p, int nwb, int* off, i
   for (int w = 0; w < warp; ++w) at += wsum[w];
   for (int e = e0; e < e1; ++e) {
     first[e] = static_cast<int>(min(at, kMaxUnits));
-    at += static_cast<int64_t>(runs_of(max(off[e + 1] - off[e], 0), p.nmax)) * nwb;
+    at += static_cast<int64_t>(runs_of<F>(max(off[e + 1] - off[e], 0))) * nwb;
   }
   // threads past the experts carry the total
   if (tid == threads - 1) first[p.E] = static_cast<int>(min(at, kMaxUnits));
@@ -123,8 +137,8 @@ __device__ __forceinline__ void unit_table(const Params& p, int nwb, int* off, i
 
 // The expert that owns unit u: the last e with first[e] <= u.  The whole warp
 // searches: 32 probes spread over the experts, then 32 at a time between two.
-template <int STEP>
-__device__ __forceinline__ Unit find_unit(const int* first, const int* off, int E, int nmax, int u, int lane) {
+template <class F>
+__device__ __forceinline__ Unit find_unit(const int* first, const int* off, int E, int u, int lane) {
   const int step = (E + 31) / 32;
   const int i = lane * step;
   const uint32_t m = __ballot_sync(0xffffffffu, i < E && first[i] <= u);
@@ -137,14 +151,14 @@ __device__ __forceinline__ Unit find_unit(const int* first, const int* off, int 
   Unit un;
   un.e = b + cnt - 1;
   const int c = off[un.e + 1] - off[un.e];
-  const int nr = runs_of(c, nmax);
-  const int per = ((c + nr - 1) / nr + STEP - 1) & ~(STEP - 1);
+  const int nr = runs_of<F>(c);
+  const int per = ((c + nr - 1) / nr + F::STEP - 1) & ~(F::STEP - 1);
   const int v = u - first[un.e];
   un.wb = v / nr;
   const int run = v - un.wb * nr;
   un.row0 = off[un.e] + run * per;
   un.rows = min(per, c - run * per);
-  un.n = (un.rows + STEP - 1) & ~(STEP - 1);
+  un.n = (un.rows + F::STEP - 1) & ~(F::STEP - 1);
   return un;
 }
 
@@ -178,6 +192,29 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, const
   const int64_t t0 = clock64();
   while (!mbar_try_wait(a, parity) && clock64() - t0 <= p.timeout_cycles) {
   }
+}
+
+// The epilogue's wait for an accumulator, of which it is a whole unit ahead:
+// one lane looks every 200 ns and the warp sleeps in between.
+__device__ __forceinline__ bool warp_nap(uint64_t* bar, uint32_t parity, int lane, volatile int* abort_flag,
+                                         const Params& p) {
+  int got = 1;
+  if (lane == 0) {
+    const uint32_t a = smem_u32(bar);
+    int64_t t0 = 0;
+    while (!mbar_try_wait(a, parity)) {
+      const int64_t now = clock64();
+      t0 = t0 == 0 ? now : t0;
+      if (*abort_flag || now - t0 > p.timeout_cycles) {
+        if (!*abort_flag) atomicOr(p.err, kDevErrTimeout);
+        *abort_flag = 1;
+        got = 0;
+        break;
+      }
+      __nanosleep(200);
+    }
+  }
+  return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
 // One lane waits, the warp learns the outcome.
@@ -217,29 +254,65 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane) {
 // 2^-11).
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// h = SiLU(g) u of this lane's feature (feat0 + lane) for 8 tokens, as MXFP4:
+// h = SiLU(g) u of this lane's feature (feat0 + lane) for 16 tokens, as MXFP4:
 // the warp's 32 features are a block.  Stores the codes and scales of rows
-// un.row0 + c .. + 7 that belong to the run.
-__device__ __forceinline__ void emit_h8(const Params& p, const Unit& un, int feat0, int c, const float (&g)[8],
-                                        const float (&u)[8], int lane) {
-  uint32_t byte = 0;      // lane j: scale byte of token c + j
-  float h[8];
+// un.row0 + c .. + 15 that belong to the run.  Two groups of 8 tokens side by
+// side, since the chain of one (special functions, exchanges) is latency.
+__device__ __forceinline__ void emit_h16(const Params& p, const Unit& un, int feat0, int c, const float (&g)[16],
+                                         const float (&u)[16], int lane) {
+  // Largest magnitude of each token over the lanes: three exchanges that halve
+  // the tokens a lane holds, two more; lanes 4 j .. 4 j + 3 end with token
+  // 8 o + j's.  (A warp reduction a token took 1440 cycles for 8 tokens where
+  // this takes 1110.)
+  float h[2][8];
+  uint32_t m[2][8], byte[2];
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[o][j] = swiglu(g[8 * o + j], u[8 * o + j]);
+      m[o][j] = __float_as_uint(h[o][j]) & 0x7FFFFFFFu;
+    }
+  }
+#pragma unroll
+  for (int n = 4; n >= 1; n >>= 1) {
+    const bool hi = lane & (4 * n);
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, hi ? m[o][j] : m[o][j + n], 4 * n);
+        m[o][j] = max(hi ? m[o][j + n] : m[o][j], other);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < 2; ++o) m[o][0] = max(m[o][0], __shfl_xor_sync(0xffffffffu, m[o][0], 2));
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    m[o][0] = max(m[o][0], __shfl_xor_sync(0xffffffffu, m[o][0], 1));
+    byte[o] = fp4_scale_byte(m[o][0]);
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    h[j] = swiglu(g[j], u[j]);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-    const uint32_t b = fp4_scale_byte(m);
-    h[j] = (b == kFp4NanScale) ? 0.0f : h[j] * fp4_inv_scale(b);
-    if (lane == j) byte = b;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const float inv = __shfl_sync(0xffffffffu, fp4_inv_scale(byte[o]), 4 * j);
+      h[o][j] = inv == 0.0f ? 0.0f : h[o][j] * inv;
+    }
   }
-  const uint32_t w = transpose_nibbles(e2m1x8(h), lane);
-  const int tok = c + (lane & 7);
-  if (tok < un.rows)
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + static_cast<size_t>(un.row0 + tok) * (p.N / 2) +
-                                 feat0 / 2 + 4 * (lane >> 3)) = w;
-  if (lane < 8 && c + lane < un.rows)
-    p.out_scales[(static_cast<size_t>(feat0 >> 7) * p.rows + un.row0 + c + lane) * 4 + ((feat0 >> 5) & 3)] =
-        static_cast<uint8_t>(byte);
+  uint8_t* codes = static_cast<uint8_t*>(p.out) + static_cast<size_t>(un.row0 + c) * (p.N >> 1) + (feat0 >> 1);
+  uint8_t* scales = p.out_scales + (static_cast<size_t>(feat0 >> 7) * p.rows + un.row0 + c) * 4 + ((feat0 >> 5) & 3);
+  uint32_t w[2];
+#pragma unroll
+  for (int o = 0; o < 2; ++o) w[o] = transpose_nibbles(e2m1x8(h[o]), lane);
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int tok = 8 * o + (lane & 7), stok = 8 * o + (lane >> 2);
+    if (c + tok < un.rows)
+      *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(tok) * (p.N >> 1) + 4 * (lane >> 3)) = w[o];
+    if ((lane & 3) == 0 && c + stok < un.rows) scales[4 * stok] = static_cast<uint8_t>(byte[o]);
+  }
 }
 
 // 16 tokens (c ..) of the accumulator at `taddr` (this warp's lane quarter,
@@ -283,44 +356,47 @@ __device__ __forceinline__ void emit_out16(const Params& p, const Unit& un, int 
 }
 
 // The MMAs of one stage: scales to tensor memory, then `steps` x 64 elements
-// of K for each of the unit's NA weight tiles (MAX_NA: those a stage has room
-// for).
-template <int NA, int MAX_NA, int NB, bool PAIR>
+// of K for each of the unit's NA weight tiles.
+template <class F, int NA, bool PAIR>
 __device__ __forceinline__ void issue_stage(uint32_t a_lo, uint32_t b_lo, uint64_t s_desc, uint32_t sf, uint32_t dcol,
-                                            int nmax, uint32_t id0, uint32_t id1, int kb, int steps) {
+                                            uint32_t id0, uint32_t id1, int kb, int steps) {
 #pragma unroll
-  for (int i = 0; i < sf_chunks(MAX_NA, NB); ++i)
-    if (i < 2 * NA || i >= 2 * MAX_NA)
+  for (int i = 0; i < F::kChunks; ++i)
+    if (i < 2 * NA || i >= 2 * F::NA)
       tc_cp_scales<PAIR>(sf + 4u * i, s_desc + static_cast<uint64_t>(i * (kChunkScales >> 4)));
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
     if (ks < steps) {
 #pragma unroll
       for (int a = 0; a < NA; ++a)
-        tc_mma_mxf4<PAIR>(dcol + static_cast<uint32_t>(a * nmax), a_lo + a * (kTile >> 4) + 2u * ks, b_lo + 2u * ks,
-                          (ks & 1) ? id1 : id0, sf + 4u * (2 * a + (ks >> 1)),
-                          sf + 4u * (2 * MAX_NA + NB * (ks >> 1)), (kb | ks) != 0);
+        tc_mma_mxf4<PAIR>(dcol + static_cast<uint32_t>(a * F::NMAX), a_lo + a * (kTile >> 4) + 2u * ks,
+                          b_lo + 2u * ks, (ks & 1) ? id1 : id0, sf + 4u * (2 * a + (ks >> 1)),
+                          sf + 4u * (2 * F::NA + F::NB * (ks >> 1)), (kb | ks) != 0);
     }
   }
 }
 
-template <int KIND, int NB>
+// Experts of up to 96 rows on average: 256 weight rows x 96 tokens a unit.
+// Shorter runs did not help the smallest experts (1 to 12 rows, 16 to 96
+// columns: within 3%), and at 64 rows 64-token runs cost 15% (two runs for
+// every second expert).
+using Single = Form<2, 96, 96, 16, 4, kEpiWarps * kStgBytes>;
+
+template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
+  using F = Single;
   constexpr bool SWIGLU = KIND == kOutSwiglu;
   constexpr int kRowsPerWb = SWIGLU ? kTileRows : kNA * kTileRows;   // weight rows between units
-  constexpr int kSf = sf_chunks(kNA, NB);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
-  const int S = p.stages;
-  const uint32_t tok_off = kNA * kTile, sc_off = tok_off + static_cast<uint32_t>(p.nmax) * 128u;
-  const uint32_t stage_bytes = sc_off + kSf * kChunkScales;   // a multiple of 1024
-  uint8_t* stg_all = smem + static_cast<size_t>(S) * stage_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpiWarps * kStgBytes);
-  uint64_t* empty = full + kMaxStages;
-  uint64_t* tfull = empty + kMaxStages;
-  uint64_t* tempty = tfull + kMaxBufs;
-  uint64_t* drain = tempty + kMaxBufs;
+  constexpr int S = F::S;
+  uint8_t* stg_all = smem + S * F::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + F::kStg);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + kBufs;
+  uint64_t* drain = tempty + kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int64_t* wsum = reinterpret_cast<int64_t*>(tmem_slot + 2);   // one per warp
@@ -333,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       mbar_init(full + s, 1 + kScaleLanes);     // the TMA warp and the lanes of the scale warps
       mbar_init(empty + s, 1);
     }
-    for (int b = 0; b < kMaxBufs; ++b) {
+    for (int b = 0; b < kBufs; ++b) {
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, kEpiWarps);
     }
@@ -349,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
   }
   chain_wait();
 
-  unit_table(p, (p.N + kRowsPerWb - 1) / kRowsPerWb, off, first, wsum);
+  unit_table<F>(p, (p.N + kRowsPerWb - 1) / kRowsPerWb, off, first, wsum);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -365,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
-      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int f0 = un.wb * kRowsPerWb;
       const int na = (!SWIGLU && f0 + kTileRows >= p.N) ? 1 : kNA;      // the second tile may lie past the weight
       const uint32_t tx = static_cast<uint32_t>(na) * kTile + static_cast<uint32_t>(un.n) * 128u;
@@ -375,13 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             ok = false;
             break;
           }
-          const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
+          const uint32_t sbase = smem_u32(smem + stage * F::kStage);
           const uint32_t fb = smem_u32(&full[stage]);
           mbar_arrive_expect_tx(&full[stage], tx);
           for (int a = 0; a < na; ++a)
             tma_load_3d_hint(sbase + a * kTile, &p.mapW[SWIGLU ? a : 0], fb, kb * 128,
                              f0 + (SWIGLU ? 0 : a * kTileRows), un.e, pol_w);
-          tma_load_rows<false>(sbase + tok_off, p.mapA, fb, kb * 128, un.row0, un.n, pol_a);
+          tma_load_rows<false>(sbase + F::kTokOff, p.mapA, fb, kb * 128, un.row0, un.n, pol_a);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -404,30 +480,30 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     int stage = 0;
     uint32_t phase = 0, count = 0;
     bool any = false, ok = true;
-    const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + tok_off);
-    const uint64_t s_lo = rows16_desc(smem_u32(smem) + sc_off);
+    const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + F::kTokOff);
+    const uint64_t s_lo = rows16_desc(smem_u32(smem) + F::kScaleOff);
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
-      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
       if (elect_one()) {
         const int na = (!SWIGLU && un.wb * kRowsPerWb + kTileRows >= p.N) ? 1 : kNA;
-        const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
-        const uint32_t bpar = (count / static_cast<uint32_t>(p.nbuf)) & 1u;
+        const int buf = static_cast<int>(count % kBufs);
+        const uint32_t bpar = (count / kBufs) & 1u;
         ok = wait_phase(&tempty[buf], bpar ^ 1u, abort_flag, p);
         tc_fence_after();
         const uint32_t id0 = idesc_mxf4(kTileRows, un.n, 0), id1 = idesc_mxf4(kTileRows, un.n, 1);
-        const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * kNA * p.nmax);
+        const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * F::NA * F::NMAX);
         for (int kb = 0; ok && kb < KB; ++kb) {
           ok = wait_phase(&full[stage], phase, abort_flag, p);
           if (!ok) break;
           tc_fence_after();
           fence_proxy_async_smem();      // scales written by cp.async are read by the tensor core
-          const uint32_t off_s = static_cast<uint32_t>(stage) * (stage_bytes >> 4);
-          const uint32_t sf = tmem_base + static_cast<uint32_t>(p.sf_base + stage * 4 * kSf);
+          const uint32_t off_s = static_cast<uint32_t>(stage) * (F::kStage >> 4);
+          const uint32_t sf = tmem_base + F::kSfBase + static_cast<uint32_t>(stage * 4 * F::kChunks);
           const int steps = min(4, (p.K - kb * kStageK) / 64);
           if (na == kNA)
-            issue_stage<kNA, kNA, NB, false>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
+            issue_stage<F, kNA, false>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, id0, id1, kb, steps);
           else
-            issue_stage<1, kNA, NB, false>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, p.nmax, id0, id1, kb, steps);
+            issue_stage<F, 1, false>(a_lo + off_s, b_lo + off_s, s_lo + off_s, sf, dcol, id0, id1, kb, steps);
           any = true;
           tc_commit(&empty[stage]);
           if (++stage == S) {
@@ -453,11 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     uint32_t phase = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < num_units; u += grid) {
-      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int f0 = un.wb * kRowsPerWb;
       // Rows past the weight or the run repeat the last one there is; their
       // results are never stored.
-      uint32_t wrow[kNA][4], trow[4 * NB];
+      uint32_t wrow[kNA][4], trow[4 * F::NB];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -465,11 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
           wrow[a][c] = static_cast<uint32_t>(min(f0 + (SWIGLU ? 0 : a * kTileRows) + 32 * c + lane, p.N - 1));
       }
 #pragma unroll
-      for (int c = 0; c < 4 * NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
+      for (int c = 0; c < 4 * F::NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
       for (int kb = 0; kb < KB; ++kb) {
         ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
         if (!ok) break;
-        const uint32_t dst = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes) + sc_off + 16u * lane;
+        const uint32_t dst = smem_u32(smem + stage * F::kStage) + F::kScaleOff + 16u * lane;
         const int kc = min(2 * kb + h, KC - 1);
         const size_t wchunk = (static_cast<size_t>(un.e) * KC + kc) * p.N;
         const uint32_t* tsrc = p.a_scales + static_cast<size_t>(kc) * p.rows;
@@ -480,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
           for (int c = 0; c < 4; ++c) cp_async_4(dst + (2 * a + h) * kChunkScales + 4 * c, wsrc + wrow[a][c]);
         }
 #pragma unroll
-        for (int c = 0; c < 4 * NB; ++c)
+        for (int c = 0; c < 4 * F::NB; ++c)
           if (32 * c < un.n)
-            cp_async_4(dst + (2 * kNA + NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
+            cp_async_4(dst + (2 * F::NA + F::NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
         cp_async_mbar_arrive_noinc(&full[stage]);
         if (++stage == S) {
           stage = 0;
@@ -493,36 +569,33 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
     cp_async_wait_all();
   } else if (warp >= kFirstEpi) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, part4 = (warp - kFirstEpi) >> 2;
+    const int q = warp & 3, part = (warp - kFirstEpi) >> 2;
     uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
     uint32_t count = 0;
     for (int u = blockIdx.x; u < num_units; u += grid, ++count) {
-      const Unit un = find_unit<16>(first, off, p.E, p.nmax, u, lane);
-      const int buf = static_cast<int>(count % static_cast<uint32_t>(p.nbuf));
-      const uint32_t bpar = (count / static_cast<uint32_t>(p.nbuf)) & 1u;
-      if (!warp_wait(&tfull[buf], bpar, lane, abort_flag, p)) break;
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
+      const int buf = static_cast<int>(count % kBufs);
+      const uint32_t bpar = (count / kBufs) & 1u;
+      if (!warp_nap(&tfull[buf], bpar, lane, abort_flag, p)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
-                          static_cast<uint32_t>(buf * kNA * p.nmax);
+                          static_cast<uint32_t>(buf * F::NA * F::NMAX);
       // column blocks of 16 tokens, every kEpiPer-th one
       if constexpr (SWIGLU) {
         const int feat0 = un.wb * kTileRows + 32 * q;
         if (feat0 < p.N) {
-          for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer) {
+          for (int c = 16 * part; c < un.n; c += 16 * kEpiPer) {
             uint32_t g[16], v[16];
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), g);
-            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(p.nmax + c), v);
+            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(F::NMAX + c), v);
             tmem_ld_wait();
+            float gate[16], up[16];
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              float gate[8], up[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                gate[j] = __uint_as_float(g[8 * o + j]);
-                up[j] = __uint_as_float(v[8 * o + j]);
-              }
-              emit_h8(p, un, feat0, c + 8 * o, gate, up, lane);
+            for (int j = 0; j < 16; ++j) {
+              gate[j] = __uint_as_float(g[j]);
+              up[j] = __uint_as_float(v[j]);
             }
+            emit_h16(p, un, feat0, c, gate, up, lane);
           }
         }
       } else {
@@ -530,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
         for (int a = 0; a < kNA; ++a) {
           const int feat0 = un.wb * kRowsPerWb + a * kTileRows + 32 * q;
           if (feat0 >= p.N) break;
-          for (int c = 16 * part4; c < un.n; c += 16 * kEpiPer)
-            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(a * p.nmax + c), stg, lane);
+          for (int c = 16 * part; c < un.n; c += 16 * kEpiPer)
+            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(a * F::NMAX + c), stg, lane);
         }
       }
       tc_fence_before();
@@ -557,37 +630,34 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 //   swiglu:  CTA r has features 64 r .. of the unit's 128, their gate rows in
 //            lanes 0..63 and their up rows in lanes 64..127.  A gate warp and
 //            the up warp of the same features exchange half of their values
-//            through shared memory, then each finishes 8 of 16 tokens.
+//            through shared memory, then each finishes 16 of 32 tokens.
 // Roles as above, in both CTAs; the MMAs are issued by the leader (rank 0)
 // for both.  cp.async can only arrive on a barrier of its own CTA, so the
 // peer's scale copies complete a barrier there, and the peer's warp 1, which
 // has no MMAs to issue, reports it to the leader's.  (A scale warp that waited
 // for its own copies and reported them itself took 1.35 us a stage: its
 // cluster-scope release waits for the copies of later stages too.)
-constexpr int kPairN = 192;
-constexpr int kPairStep = 32;                             // runs are multiples of this: half per CTA
-constexpr uint32_t kXchBytes = 2 * 2 * 32 * 8 * 4;        // per warp pair: 2 buffers x 2 directions x 32 lanes x 8 floats
+constexpr uint32_t kXchBytes = 2 * 2 * 32 * 16 * 4;       // per warp pair: 2 buffers x 2 directions x 32 lanes x 16 floats
+
+using Pair = Form<1, 192, 96, 32, 5, kEpiWarps / 2 * kXchBytes>;
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp4_gemm_pair_kernel(const __grid_constant__ Params p) {
+  using F = Pair;
   constexpr bool SWIGLU = KIND == kOutSwiglu;
   constexpr int kCtaFeats = SWIGLU ? kTileRows / 2 : kTileRows;      // output features per CTA
   constexpr int kRowsPerWb = 2 * kCtaFeats;
-  constexpr int NB = 2;
-  constexpr int kSf = sf_chunks(1, NB);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
-  const int S = p.stages;
-  const uint32_t tok_off = kTile, sc_off = tok_off + static_cast<uint32_t>(p.nmax / 2) * 128u;
-  const uint32_t stage_bytes = sc_off + kSf * kChunkScales;          // a multiple of 1024
-  uint8_t* stg_all = smem + static_cast<size_t>(S) * stage_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kPairStgBytes);
-  uint64_t* empty = full + kMaxStages;
-  uint64_t* tfull = empty + kMaxStages;
-  uint64_t* tempty = tfull + kMaxBufs;
-  uint64_t* drain = tempty + kMaxBufs;
+  constexpr int S = F::S;
+  uint8_t* stg_all = smem + S * F::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + F::kStg);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + kBufs;
+  uint64_t* drain = tempty + kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int64_t* wsum = reinterpret_cast<int64_t*>(tmem_slot + 2);
@@ -604,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(full + s, rank == 0 ? 2 + kScaleLanes + 1 : kScaleLanes);
       mbar_init(empty + s, 1);
     }
-    for (int b = 0; b < kMaxBufs; ++b) {
+    for (int b = 0; b < kBufs; ++b) {
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, 2 * kEpiWarps);
     }
@@ -619,7 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
   chain_wait();
-  unit_table(p, (p.N + kRowsPerWb - 1) / kRowsPerWb, off, first, wsum);
+  unit_table<F>(p, (p.N + kRowsPerWb - 1) / kRowsPerWb, off, first, wsum);
   tc_fence_before();
   __syncthreads();
   cluster_sync();                        // the peer's barriers are initialised
@@ -637,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int u = pair; ok && u < num_units; u += npairs) {
-      const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
       const int half = un.n >> 1, row0 = un.row0 + static_cast<int>(rank) * half;
       const uint32_t tx = kTile + static_cast<uint32_t>(half) * 128u;
@@ -647,12 +717,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t sbase = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes);
+          const uint32_t sbase = smem_u32(smem + stage * F::kStage);
           const uint32_t fb = full_leader + 8u * stage;
           mbar_arrive_expect_tx_cluster(fb, tx);
           tma_load_3d_pair_hint(sbase, &p.mapW[0], fb, kb * 128, f0, un.e, pol_w);
           if (SWIGLU) tma_load_3d_pair_hint(sbase + kTile / 2, &p.mapW[1], fb, kb * 128, f0, un.e, pol_w);
-          tma_load_rows<true>(sbase + tok_off, p.mapA, fb, kb * 128, row0, half, pol_a);
+          tma_load_rows<true>(sbase + F::kTokOff, p.mapA, fb, kb * 128, row0, half, pol_a);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -676,26 +746,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0, count = 0;
       bool any = false, ok = true;
-      const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + tok_off);
-      const uint64_t s_lo = rows16_desc(smem_u32(smem) + sc_off);
+      const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + F::kTokOff);
+      const uint64_t s_lo = rows16_desc(smem_u32(smem) + F::kScaleOff);
       for (int u = pair; ok && u < num_units; u += npairs) {
-        const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+        const Unit un = find_unit<F>(first, off, p.E, u, lane);
         if (elect_one()) {
-          const int buf = static_cast<int>(count % kMaxBufs);
-          const uint32_t bpar = (count / kMaxBufs) & 1u;
+          const int buf = static_cast<int>(count % kBufs);
+          const uint32_t bpar = (count / kBufs) & 1u;
           ok = wait_phase(&tempty[buf], bpar ^ 1u, abort_flag, p);
           tc_fence_after();
           const uint32_t id0 = idesc_mxf4(2 * kTileRows, un.n, 0), id1 = idesc_mxf4(2 * kTileRows, un.n, 1);
-          const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * p.nmax);
+          const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * F::NMAX);
           for (int kb = 0; ok && kb < KB; ++kb) {
             ok = wait_phase(&full[stage], phase, abort_flag, p);
             if (!ok) break;
             tc_fence_after();
             fence_proxy_async_smem();
-            const uint32_t off_s = static_cast<uint32_t>(stage) * (stage_bytes >> 4);
-            issue_stage<1, 1, NB, true>(a_lo + off_s, b_lo + off_s, s_lo + off_s,
-                                        tmem_base + static_cast<uint32_t>(p.sf_base + stage * 4 * kSf), dcol, p.nmax,
-                                        id0, id1, kb, min(4, (p.K - kb * kStageK) / 64));
+            const uint32_t off_s = static_cast<uint32_t>(stage) * (F::kStage >> 4);
+            issue_stage<F, 1, true>(a_lo + off_s, b_lo + off_s, s_lo + off_s,
+                                    tmem_base + F::kSfBase + static_cast<uint32_t>(stage * 4 * F::kChunks), dcol, id0,
+                                    id1, kb, min(4, (p.K - kb * kStageK) / 64));
             any = true;
             tc_commit_pair(&empty[stage], 0x3);
             if (++stage == S) {
@@ -742,30 +812,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; ok && u < num_units; u += npairs) {
-      const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
       // Rows past the weight or the run repeat the last one there is; their
       // results are never stored.
       const uint32_t* wsrc[4];
-      uint32_t trow[4 * NB];
+      uint32_t trow[4 * F::NB];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int r = SWIGLU ? f0 + 32 * (c & 1) + lane : f0 + 32 * c + lane;
         wsrc[c] = p.w_scales[SWIGLU ? c >> 1 : 0] + static_cast<size_t>(un.e) * KC * p.N + min(r, p.N - 1);
       }
 #pragma unroll
-      for (int c = 0; c < 4 * NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
+      for (int c = 0; c < 4 * F::NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
       for (int kb = 0; kb < KB; ++kb) {
         ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
         if (!ok) break;
-        const uint32_t dst = smem_u32(smem + static_cast<size_t>(stage) * stage_bytes) + sc_off + 16u * lane;
+        const uint32_t dst = smem_u32(smem + stage * F::kStage) + F::kScaleOff + 16u * lane;
         const int kc = min(2 * kb + h, KC - 1);
         const uint32_t* tsrc = p.a_scales + static_cast<size_t>(kc) * p.rows;
 #pragma unroll
         for (int c = 0; c < 4; ++c) cp_async_4(dst + h * kChunkScales + 4 * c, wsrc[c] + static_cast<size_t>(kc) * p.N);
 #pragma unroll
-        for (int c = 0; c < 4 * NB; ++c)
-          if (32 * c < un.n) cp_async_4(dst + (2 + NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
+        for (int c = 0; c < 4 * F::NB; ++c)
+          if (32 * c < un.n) cp_async_4(dst + (2 * F::NA + F::NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
         cp_async_mbar_arrive_noinc(&full[stage]);
         if (++stage == S) {
           stage = 0;
@@ -776,69 +846,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cp_async_wait_all();
   } else if (warp >= kFirstEpi) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, part2 = (warp - kFirstEpi) >> 2;
+    const int q = warp & 3, part = (warp - kFirstEpi) >> 2;
     uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
     // swiglu: lane quarters q and q ^ 2 hold gate and up of the same features
-    const int wp = 2 * part2 + (q & 1);
+    const int wp = 2 * part + (q & 1);
     float4* xch = reinterpret_cast<float4*>(stg_all + wp * kXchBytes);
     volatile int* vote = reinterpret_cast<volatile int*>(wsum + kThreads / 32) + 2 * wp;
     uint32_t count = 0;
     int turn = 0;
     for (int u = pair; u < num_units; u += npairs, ++count) {
-      const Unit un = find_unit<kPairStep>(first, off, p.E, p.nmax, u, lane);
-      const int buf = static_cast<int>(count % kMaxBufs);
-      const uint32_t bpar = (count / kMaxBufs) & 1u;
-      bool got_acc = warp_wait(&tfull[buf], bpar, lane, abort_flag, p);
+      const Unit un = find_unit<F>(first, off, p.E, u, lane);
+      const int buf = static_cast<int>(count % kBufs);
+      const uint32_t bpar = (count / kBufs) & 1u;
+      bool got_acc = warp_nap(&tfull[buf], bpar, lane, abort_flag, p);
       if constexpr (SWIGLU) {
         // Both warps of an exchange go on, or neither does: they meet at its
         // barriers.  The slots of a unit are written again two units later.
-        volatile int* v = vote + 8 * (count & 1);
+        volatile int* v = vote + kEpiWarps * (count & 1);
         if (lane == 0) v[q >> 1] = got_acc;
         named_barrier(1 + wp, 64);
         got_acc = got_acc && v[1 - (q >> 1)] != 0;
       }
       if (!got_acc) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * p.nmax);
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * F::NMAX);
       const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
       const int feat0 = f0 + 32 * (SWIGLU ? q & 1 : q);
       if (feat0 < p.N) {
-        for (int c = 16 * part2; c < un.n; c += 16 * kEpiPer) {
-          if constexpr (SWIGLU) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v);
+        if constexpr (SWIGLU) {
+          // 32 tokens at a time: the gate warp keeps 0..15 and gives away
+          // 16..31, the up warp the other way round
+          const bool up = q >= 2;
+          for (int c = 32 * part; c < un.n; c += 32 * kEpiPer) {
+            uint32_t v[2][16];
+            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v[0]);
+            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c + 16), v[1]);
             tmem_ld_wait();
-            // the gate warp gives away tokens 8..15 and the up warp 0..7
-            const bool up = q >= 2;
-            float4* give = xch + (2 * turn + (up ? 1 : 0)) * 64;
-            const float4* take = xch + (2 * turn + (up ? 0 : 1)) * 64;
-            float keep[8], got[8];
+            float4* give = xch + (2 * turn + (up ? 1 : 0)) * 128;
+            const float4* take = xch + (2 * turn + (up ? 0 : 1)) * 128;
+            float keep[16], got[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) keep[j] = __uint_as_float(up ? v[8 + j] : v[j]);
+            for (int j = 0; j < 16; ++j) keep[j] = __uint_as_float(up ? v[1][j] : v[0][j]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              give[32 * j + lane] =
-                  up ? make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                   __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]))
-                     : make_float4(__uint_as_float(v[8 + 4 * j]), __uint_as_float(v[9 + 4 * j]),
-                                   __uint_as_float(v[10 + 4 * j]), __uint_as_float(v[11 + 4 * j]));
+            for (int j = 0; j < 16; j += 4)
+              give[8 * j + lane] = make_float4(__uint_as_float(up ? v[0][j] : v[1][j]),
+                                               __uint_as_float(up ? v[0][j + 1] : v[1][j + 1]),
+                                               __uint_as_float(up ? v[0][j + 2] : v[1][j + 2]),
+                                               __uint_as_float(up ? v[0][j + 3] : v[1][j + 3]));
             named_barrier(1 + wp, 64);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 f = take[32 * j + lane];
-              got[4 * j] = f.x;
-              got[4 * j + 1] = f.y;
-              got[4 * j + 2] = f.z;
-              got[4 * j + 3] = f.w;
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = take[8 * j + lane];
+              got[j] = f.x;
+              got[j + 1] = f.y;
+              got[j + 2] = f.z;
+              got[j + 3] = f.w;
             }
             turn ^= 1;                   // the other buffer next: one barrier a block suffices
-            if (up)
-              emit_h8(p, un, feat0, c + 8, got, keep, lane);
-            else
-              emit_h8(p, un, feat0, c, keep, got, lane);
-          } else {
-            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(c), stg, lane);
+            float gate[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              gate[j] = up ? got[j] : keep[j];
+              got[j] = up ? keep[j] : got[j];
+            }
+            emit_h16(p, un, feat0, up ? c + 16 : c, gate, got, lane);
           }
+        } else {
+          for (int c = 16 * part; c < un.n; c += 16 * kEpiPer)
+            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(c), stg, lane);
         }
       }
       tc_fence_before();
@@ -872,57 +947,32 @@ bool map_weight(CUtensorMap* m, const void* codes, int E, int N, int K, int rows
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int KIND, int NB>
-int launch_single(const Params& prm, int grid, size_t smem, cudaStream_t st) {
-  static std::atomic<int> limit[64];
-  const int rc = raise_smem_limit(fp4_gemm_kernel<KIND, NB>, limit, static_cast<int>(smem));
+// Both forms of one kind: the function launched, its grid and shared memory.
+template <int KIND>
+int launch_kind(const Params& prm, bool pair, int sms, cudaStream_t st) {
+  static std::atomic<int> single_limit[64], pair_limit[64];
+  const auto kern = pair ? fp4_gemm_pair_kernel<KIND> : fp4_gemm_kernel<KIND>;
+  const uint32_t fixed = pair ? Pair::kFixed : Single::kFixed, tables = 2u * 4u * (kMaxE + 1);
+  const int rc = raise_smem_limit(kern, pair ? pair_limit : single_limit, static_cast<int>(fixed + tables));
   if (rc != MOE_OK) return rc;
-  return launch_chained(fp4_gemm_kernel<KIND, NB>, dim3(grid), dim3(kThreads), smem, st, prm) == cudaSuccess
+  const size_t smem = fixed + 2 * 4 * (static_cast<size_t>(prm.E) + 1);
+  return launch_chained(kern, dim3(pair ? sms & ~1 : sms), dim3(kThreads), smem, st, prm) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
-}
-
-template <int KIND>
-int launch_pair(const Params& prm, int grid, size_t smem, cudaStream_t st) {
-  static std::atomic<int> limit[64];
-  const int rc = raise_smem_limit(fp4_gemm_pair_kernel<KIND>, limit, static_cast<int>(smem));
-  if (rc != MOE_OK) return rc;
-  return launch_chained(fp4_gemm_pair_kernel<KIND>, dim3(grid & ~1), dim3(kThreads), smem, st, prm) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
-}
-
-template <int KIND>
-int launch_kind(const Params& prm, bool pair, bool wide, int grid, size_t smem, cudaStream_t st) {
-  if (pair) return launch_pair<KIND>(prm, grid, smem, st);
-  return wide ? launch_single<KIND, 2>(prm, grid, smem, st) : launch_single<KIND, 1>(prm, grid, smem, st);
 }
 
 }  // namespace
 
 int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err, cudaStream_t st) {
   const bool swiglu = q.w1_codes != nullptr;
-  Params p;
-  // Rows per run: the smallest step that holds the average expert.
+  // CTA pairs above 96 rows an expert, what a single CTA's unit takes in one
+  // run.  64 experts of 104 / 128 / 160 / 512 rows, pairs against single CTAs:
+  // N = 4096, K = 1024 product 38 / 43 / 47 / 123 us against 43 / 48 / 52 / 142;
+  // f = 1024, K = 4096 gate/up 60 / 64 / 70 / 186 against 66 / 71 / 75 / 210.
+  // 256 experts of 96 / 64 rows: 259 / 240 against 241 / 203 (gate/up).
   const int64_t avg = (static_cast<int64_t>(q.rows) + q.E - 1) / q.E;
-  bool pair = avg > 64 && di.sms >= 2;
-  p.nmax = avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : pair ? kPairN : 96;
-  p.nbuf = 2;
-  const bool wide = p.nmax > kTileRows;
-  // Stages: what shared memory and (accumulators first) tensor memory hold.
-  const int na = pair ? 1 : kNA, chunks = sf_chunks(na, wide ? 2 : 1);
-  const size_t fixed = kSmemAlign + (pair ? kPairStgBytes : kEpiWarps * kStgBytes) + kSmemTail +
-                       2 * (static_cast<size_t>(q.E) + 1) * 4;
-  const size_t stage = na * kTile + static_cast<size_t>(pair ? p.nmax / 2 : p.nmax) * 128 + chunks * kChunkScales;
-  const int acc = p.nbuf * na * p.nmax;
-  p.stages = static_cast<int>((kSmemBudget - fixed) / stage);
-  p.stages = p.stages < kMaxStages ? p.stages : kMaxStages;
-  const int sf_stages = (static_cast<int>(kTmemCols) - acc) / (4 * chunks);
-  p.stages = p.stages < sf_stages ? p.stages : sf_stages;
-  if (p.stages < 2) return MOE_ERR_UNSUPPORTED;
-  p.sf_base = static_cast<int>(kTmemCols) - p.stages * 4 * chunks;
-  const size_t smem = fixed + p.stages * stage;
-
+  const bool pair = avg > Single::NMAX && di.sms >= 2;
+  Params p;
   const int wrows = pair && swiglu ? kTileRows / 2 : kTileRows;
   for (int a = 0; a < kNA; ++a) {
     const bool second = swiglu && a == 1;
@@ -946,12 +996,11 @@ int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err,
   p.N = q.N;
   p.K = q.K;
   p.timeout_cycles = 2 * static_cast<int64_t>(kWaitTimeoutNs);   // at up to 2 GHz: 2 s or more
-  const int grid = di.sms;
-  if (swiglu) return launch_kind<kOutSwiglu>(p, pair, wide, grid, smem, st);
+  if (swiglu) return launch_kind<kOutSwiglu>(p, pair, di.sms, st);
   switch (q.dtype) {
-    case MOE_BF16: return launch_kind<kOutBf16>(p, pair, wide, grid, smem, st);
-    case MOE_FP16: return launch_kind<kOutFp16>(p, pair, wide, grid, smem, st);
-    default: return launch_kind<kOutFp32>(p, pair, wide, grid, smem, st);
+    case MOE_BF16: return launch_kind<kOutBf16>(p, pair, di.sms, st);
+    case MOE_FP16: return launch_kind<kOutFp16>(p, pair, di.sms, st);
+    default: return launch_kind<kOutFp32>(p, pair, di.sms, st);
   }
 }
 
