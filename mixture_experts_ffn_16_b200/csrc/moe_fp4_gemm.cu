@@ -79,10 +79,10 @@ struct Unit {
 };
 
 // Layout of a kernel: NA weight tiles of 128 rows and TOK token rows a stage,
-// S stages, runs of up to NMAX tokens in multiples of STEP.
-template <int NA_, int NMAX_, int TOK_, int STEP_, int S_, uint32_t STG_>
+// S stages, runs of up to NMAX tokens.
+template <int NA_, int NMAX_, int TOK_, int S_, uint32_t STG_>
 struct Form {
-  static constexpr int NA = NA_, NMAX = NMAX_, STEP = STEP_, S = S_;
+  static constexpr int NA = NA_, NMAX = NMAX_, S = S_;
   static constexpr int NB = (NMAX + kTileRows - 1) / kTileRows;    // 128s of tokens
   // Scales of one stage: 2 chunks of 128 elements for each 128 rows of the
   // weight tiles, then of the run; 4 columns of tensor memory each.
@@ -152,13 +152,13 @@ __device__ __forceinline__ Unit find_unit(const int* first, const int* off, int 
   un.e = b + cnt - 1;
   const int c = off[un.e + 1] - off[un.e];
   const int nr = runs_of<F>(c);
-  const int per = ((c + nr - 1) / nr + F::STEP - 1) & ~(F::STEP - 1);
+  const int per = ((c + nr - 1) / nr + 15) & ~15;
   const int v = u - first[un.e];
   un.wb = v / nr;
   const int run = v - un.wb * nr;
   un.row0 = off[un.e] + run * per;
   un.rows = min(per, c - run * per);
-  un.n = (un.rows + F::STEP - 1) & ~(F::STEP - 1);
+  un.n = (un.rows + 15) & ~15;
   return un;
 }
 
@@ -380,7 +380,7 @@ __device__ __forceinline__ void issue_stage(uint32_t a_lo, uint32_t b_lo, uint64
 // Shorter runs did not help the smallest experts (1 to 12 rows, 16 to 96
 // columns: within 3%), and at 64 rows 64-token runs cost 15% (two runs for
 // every second expert).
-using Single = Form<2, 96, 96, 16, 4, kEpiWarps * kStgBytes>;
+using Single = Form<2, 96, 96, 4, kEpiWarps * kStgBytes>;
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 // cluster-scope release waits for the copies of later stages too.)
 constexpr uint32_t kXchBytes = 2 * 2 * 32 * 16 * 4;       // per warp pair: 2 buffers x 2 directions x 32 lanes x 16 floats
 
-using Pair = Form<1, 192, 96, 32, 5, kEpiWarps / 2 * kXchBytes>;
+using Pair = Form<1, 192, 96, 5, kEpiWarps / 2 * kXchBytes>;
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -709,8 +709,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int u = pair; ok && u < num_units; u += npairs) {
       const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
-      const int half = un.n >> 1, row0 = un.row0 + static_cast<int>(rank) * half;
-      const uint32_t tx = kTile + static_cast<uint32_t>(half) * 128u;
+      // Half of the run, a multiple of 8 rows; loaded as a multiple of 16.
+      const int half = un.n >> 1, row0 = un.row0 + static_cast<int>(rank) * half, load = (half + 15) & ~15;
+      const uint32_t tx = kTile + static_cast<uint32_t>(load) * 128u;
       if (elect_one()) {
         for (int kb = 0; kb < KB; ++kb) {
           if (!wait_phase(&empty[stage], phase ^ 1u, abort_flag, p)) {
@@ -722,7 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx_cluster(fb, tx);
           tma_load_3d_pair_hint(sbase, &p.mapW[0], fb, kb * 128, f0, un.e, pol_w);
           if (SWIGLU) tma_load_3d_pair_hint(sbase + kTile / 2, &p.mapW[1], fb, kb * 128, f0, un.e, pol_w);
-          tma_load_rows<true>(sbase + F::kTokOff, p.mapA, fb, kb * 128, row0, half, pol_a);
+          tma_load_rows<true>(sbase + F::kTokOff, p.mapA, fb, kb * 128, row0, load, pol_a);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -875,7 +876,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (feat0 < p.N) {
         if constexpr (SWIGLU) {
           // 32 tokens at a time: the gate warp keeps 0..15 and gives away
-          // 16..31, the up warp the other way round
+          // 16..31, the up warp the other way round (columns past the run
+          // hold what they held; their rows are not stored)
           const bool up = q >= 2;
           for (int c = 32 * part; c < un.n; c += 32 * kEpiPer) {
             uint32_t v[2][16];
