@@ -23,31 +23,76 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 q = __bfloat1622float2(h[i]);
-    f[2 * i] = q.x;
-    f[2 * i + 1] = q.y;
+// Eight elements as they lie in memory: their largest magnitude as float bits
+// (NaN above infinity above every number) and their multiples by a power of
+// two.  16-bit types stay packed for the first, bf16 for both: the scaled
+// value is exact in bf16, or so small (below 2^-126) that it rounds to 0.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
-}
-__device__ __forceinline__ void load8(const __half* p, float (&f)[8]) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-  const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 q = __half22float2(h[i]);
-    f[2 * i] = q.x;
-    f[2 * i + 1] = q.y;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    const uint32_t k = 0x7FFFFFFFu;
+    return max(max(max(__float_as_uint(a.x) & k, __float_as_uint(a.y) & k),
+                   max(__float_as_uint(a.z) & k, __float_as_uint(a.w) & k)),
+               max(max(__float_as_uint(b.x) & k, __float_as_uint(b.y) & k),
+                   max(__float_as_uint(b.z) & k, __float_as_uint(b.w) & k)));
   }
-}
+  __device__ __forceinline__ void times(float s, float (&f)[8]) const {
+    f[0] = a.x * s; f[1] = a.y * s; f[2] = a.z * s; f[3] = a.w * s;
+    f[4] = b.x * s; f[5] = b.y * s; f[6] = b.z * s; f[7] = b.w * s;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  __nv_bfloat162 h[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    *reinterpret_cast<uint4*>(h) = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(h) = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                                         __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+    return max(w << 16, w & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void times(float s, float (&f)[8]) const {
+    const __nv_bfloat162 s2 = __float2bfloat162_rn(s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = __bfloat1622float2(__hmul2(h[i], s2));
+      f[2 * i] = q.x;
+      f[2 * i + 1] = q.y;
+    }
+  }
+};
+template <>
+struct Eight<__half> {
+  __half2 h[4];
+  __device__ __forceinline__ void load(const __half* p) {
+    *reinterpret_cast<uint4*>(h) = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(h) = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    const float2 m = __half22float2(__hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                                                __hmax2_nan(__habs2(h[2]), __habs2(h[3]))));
+    return max(__float_as_uint(m.x), __float_as_uint(m.y));
+  }
+  __device__ __forceinline__ void times(float s, float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = __half22float2(h[i]);
+      f[2 * i] = q.x * s;
+      f[2 * i + 1] = q.y * s;
+    }
+  }
+};
 __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
@@ -74,10 +119,9 @@ constexpr int kWarpGroups = 32 * kUnits;
 // the 16 lanes' 128 elements (every lane of the 16 gets it).  All lanes of the
 // warp take part; a lane behind the row's end passes zeros, and its byte of
 // the word is 0.
-__device__ __forceinline__ uint32_t quantize8(float (&f)[8], uint32_t* word) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+template <typename T>
+__device__ __forceinline__ uint32_t quantize8(const Eight<T>& x, uint32_t* word) {
+  uint32_t m = x.amax_bits();
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const uint32_t byte = fp4_scale_byte(m);
@@ -85,11 +129,9 @@ __device__ __forceinline__ uint32_t quantize8(float (&f)[8], uint32_t* word) {
   w |= __shfl_xor_sync(0xffffffffu, w, 4);
   w |= __shfl_xor_sync(0xffffffffu, w, 8);
   *word = w;
-  if (byte == kFp4NanScale) return 0u;
-  const float inv = fp4_inv_scale(byte);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] *= inv;
-  return e2m1x8(f);
+  float f[8];
+  x.times(fp4_inv_scale(byte), f);
+  return byte == kFp4NanScale ? 0u : e2m1x8(f);
 }
 
 // 4 x 4 words between the four lanes of a block: lane i gets word i of lanes
@@ -127,9 +169,11 @@ struct Layout {
   int P, groups, chunks, per_matrix;     // groups = K / 8; rows per matrix
 };
 
+// The groups of one warp: they start at group rem0 of row row0.
 struct Span {
   int64_t row0;
   uint32_t rem0;
+  int left;          // rows from row0 on (capped)
 };
 __device__ __forceinline__ Span warp_span(const Layout& l) {
   const uint64_t first =
@@ -137,14 +181,16 @@ __device__ __forceinline__ Span warp_span(const Layout& l) {
   Span s;
   s.row0 = static_cast<int64_t>(__umul64hi(first, l.m64));
   s.rem0 = static_cast<uint32_t>(first - static_cast<uint64_t>(s.row0) * l.P);
+  s.left = static_cast<int>(min(max(l.rows - s.row0, static_cast<int64_t>(0)), static_cast<int64_t>(kWarpGroups)));
   return s;
 }
-// Group `o` of the warp's: its row and its place in the row.
-__device__ __forceinline__ void locate(const Layout& l, const Span& s, int o, int64_t* row, int* u) {
+// Group `o` of the warp's: its row, counted from row0, and its place in the
+// row; false behind the last row.
+__device__ __forceinline__ bool locate(const Layout& l, const Span& s, int o, int* dr, int* u) {
   const uint32_t t = s.rem0 + static_cast<uint32_t>(o);
-  const uint32_t dr = __umulhi(t, l.m32);
-  *row = s.row0 + dr;
-  *u = static_cast<int>(t - dr * static_cast<uint32_t>(l.P));
+  *dr = static_cast<int>(__umulhi(t, l.m32));
+  *u = static_cast<int>(t) - *dr * l.P;
+  return *dr < s.left;
 }
 // Word index of chunk c of row r in the scales.
 __device__ __forceinline__ int64_t scale_at(const Layout& l, int64_t row, int chunk) {
@@ -162,18 +208,15 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
   chain_wait();
   const int lane = threadIdx.x & 31;
   const Span s = warp_span(l);
-  float f[kUnits][8];
+  const T* x0 = x + s.row0 * l.groups * 8;
+  Eight<T> f[kUnits];
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    int64_t row;
-    int u;
-    locate(l, s, 32 * j + lane, &row, &u);
-    if (row < l.rows && u < l.groups) {
-      load8(x + (row * l.groups + u) * 8, f[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[j][i] = 0.0f;
-    }
+    int dr, u;
+    if (locate(l, s, 32 * j + lane, &dr, &u) && u < l.groups)
+      f[j].load(x0 + (dr * l.groups + u) * 8);
+    else
+      f[j].zero();
   }
   uint32_t w[kUnits], word = 0;       // word: lanes 0..7, the scales of the warp's chunk `lane`
 #pragma unroll
@@ -186,24 +229,25 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
   }
   transpose4(w);
   const uint4 block = make_uint4(w[0], w[1], w[2], w[3]);
-  int64_t brow, srow;
-  int bu, su;
-  locate(l, s, 32 * (lane & 3) + (lane & ~3), &brow, &bu);      // this lane's block of 32
-  locate(l, s, 16 * (lane & 7), &srow, &su);                    // and, lanes 0..7, chunk of 128
-  const bool bin = brow < l.rows && bu < l.groups, sin = lane < 8 && srow < l.rows;
+  int bdr, bu, sdr, su;
+  const bool bin = locate(l, s, 32 * (lane & 3) + (lane & ~3), &bdr, &bu) && bu < l.groups;   // this lane's block of 32
+  const bool sin = locate(l, s, 16 * (lane & 7), &sdr, &su) && lane < 8;                      // lanes 0..7: chunk of 128
+  const int64_t brow = s.row0 + bdr, srow = s.row0 + sdr;
   if constexpr (SLOTS) {
     const uint32_t R = static_cast<uint32_t>(l.rows) * static_cast<uint32_t>(k);
     const int32_t* bto = slot_row + brow * k;
     const int32_t* sto = slot_row + srow * k;
+    uint4* const c0 = codes + (bu >> 2);
+    uint32_t* const s0 = scales + static_cast<size_t>(su >> 4) * R;
 #pragma unroll 4
     for (int j = 0; j < k; ++j) {
       if (bin) {
         const uint32_t r = static_cast<uint32_t>(__ldg(bto + j));
-        if (r < R) codes[(static_cast<size_t>(r) * l.groups + bu) >> 2] = block;
+        if (r < R) c0[static_cast<size_t>(r) * (l.groups >> 2)] = block;
       }
       if (sin) {
         const uint32_t r = static_cast<uint32_t>(__ldg(sto + j));
-        if (r < R) scales[static_cast<size_t>(su >> 4) * R + r] = word;
+        if (r < R) s0[r] = word;
       }
     }
   } else {
@@ -219,24 +263,23 @@ dequantize_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ 
   chain_wait();
   const int lane = threadIdx.x & 31;
   const Span s = warp_span(l);
-  int64_t brow;
-  int bu;
-  locate(l, s, 32 * (lane & 3) + (lane & ~3), &brow, &bu);      // the block of 32 this lane loads
+  int bdr, bu;                                                  // the block of 32 this lane loads
+  const bool bin = locate(l, s, 32 * (lane & 3) + (lane & ~3), &bdr, &bu) && bu < l.groups;
   uint32_t w[kUnits] = {0, 0, 0, 0}, byte = 0;
-  if (brow < l.rows && bu < l.groups) {
+  if (bin) {
+    const int64_t brow = s.row0 + bdr;
     const uint4 v = __ldg(codes + ((brow * l.groups + bu) >> 2));
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     byte = (__ldg(scales + scale_at(l, brow, bu >> 4)) >> (8 * ((bu >> 2) & 3))) & 255u;
   }
   transpose4(w);                                                // unit j: group 32 j + lane
+  T* x0 = x + s.row0 * l.groups * 8;
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
     // unit j of this lane lies in the block that lane (lane & ~3) + j loaded
     const float sc = fp4_scale(__shfl_sync(0xffffffffu, byte, (lane & ~3) + j));
-    int64_t row;
-    int u;
-    locate(l, s, 32 * j + lane, &row, &u);
-    if (row < l.rows && u < l.groups) {
+    int dr, u;
+    if (locate(l, s, 32 * j + lane, &dr, &u) && u < l.groups) {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -245,7 +288,7 @@ dequantize_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ 
         f[2 * i] = q.x * sc;
         f[2 * i + 1] = q.y * sc;
       }
-      store8(x + (row * l.groups + u) * 8, f);
+      store8(x0 + (dr * l.groups + u) * 8, f);
     }
   }
 }
