@@ -478,22 +478,30 @@ def _dtype(t, name):
     return dt
 
 
-def _dev():
-    """The device the library launches on."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+def _dev(t):
+    """The device of a call whose first tensor is t: it has to be the current one, where the library launches."""
+    dev = t.get_device()
+    if dev >= 0 and dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
 def _t(t, dtype, shape, name, dev):
     """Address of a contiguous tensor of this type and shape (None: any) on device `dev`."""
     if (type(t) is torch.Tensor and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()
-            and t.get_device() == dev and dev >= 0):
+            and t.get_device() == dev >= 0):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     _p(t, dtype, shape, name)
     if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+        raise ValueError(f"{name}: on {t.device}, other tensors on cuda:{dev}")
     return t.data_ptr()
+
+
+def _on(stream, dev):
+    """The stream's handle; None: the current stream of device `dev`, without a Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _fp4_dims(q, name):
@@ -512,89 +520,89 @@ def moe_sort_tokens(topk_idx, offsets, slot_row, workspace, stream=None):
     """Rows of the (token, slot) pairs in expert order: offsets [E+1], slot_row [T, k] (-1: no expert)."""
     T, k = _dims(topk_idx, 2, "topk_idx")
     E = _dims(offsets, 1, "offsets")[0] - 1
-    dev, i32 = _dev(), torch.int32
+    dev, i32 = _dev(topk_idx), torch.int32
     _check(load().moe_sort_tokens(T, k, E, _t(topk_idx, i32, None, "topk_idx", dev),
                                   _t(offsets, i32, None, "offsets", dev), _t(slot_row, i32, (T, k), "slot_row", dev),
                                   _t(workspace, torch.uint8, None, "workspace", dev), workspace.numel(),
-                                  _stream(stream)), "moe_sort_tokens")
+                                  _on(stream, dev)), "moe_sort_tokens")
 
 
 def moe_dispatch(x, slot_row, x_sorted, stream=None):
     """x_sorted[slot_row[t, j]] = x[t]."""
     (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
-    dev, dt = _dev(), _dtype(x, "x")
+    dev, dt = _dev(x), _dtype(x, "x")
     _check(load().moe_dispatch(T, k, d, dt, _t(x, x.dtype, None, "x", dev),
                                _t(slot_row, torch.int32, (T, k), "slot_row", dev),
-                               _t(x_sorted, x.dtype, (T * k, d), "x_sorted", dev), _stream(stream)), "moe_dispatch")
+                               _t(x_sorted, x.dtype, (T * k, d), "x_sorted", dev), _on(stream, dev)), "moe_dispatch")
 
 
 def moe_dispatch_backward(dx_sorted, slot_row, dx, stream=None):
     """dx[t] = sum_j dx_sorted[slot_row[t, j]]."""
     (T, d), k = _dims(dx, 2, "dx"), _dims(slot_row, 2, "slot_row")[1]
-    dev, dt = _dev(), _dtype(dx, "dx")
+    dev, dt = _dev(dx), _dtype(dx, "dx")
     _check(load().moe_dispatch_backward(T, k, d, dt, _t(dx_sorted, dx.dtype, (T * k, d), "dx_sorted", dev),
                                         _t(slot_row, torch.int32, (T, k), "slot_row", dev),
-                                        _t(dx, dx.dtype, None, "dx", dev), _stream(stream)), "moe_dispatch_backward")
+                                        _t(dx, dx.dtype, None, "dx", dev), _on(stream, dev)), "moe_dispatch_backward")
 
 
 def moe_undispatch(y, slot_row, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] y[slot_row[t, j]]."""
     (T, d), k = _dims(out, 2, "out"), _dims(slot_row, 2, "slot_row")[1]
-    dev, dt = _dev(), _dtype(out, "out")
+    dev, dt = _dev(out), _dtype(out, "out")
     _check(load().moe_undispatch(T, k, d, dt, _t(y, out.dtype, (T * k, d), "y", dev),
                                  _t(slot_row, torch.int32, (T, k), "slot_row", dev),
                                  _t(topk_w, torch.float32, (T, k), "topk_w", dev), _t(out, out.dtype, None, "out", dev),
-                                 _stream(stream)), "moe_undispatch")
+                                 _on(stream, dev)), "moe_undispatch")
 
 
 def moe_undispatch_backward(dout, y, slot_row, topk_w, dy, dw, stream=None):
     """dy[slot_row[t, j]] = topk_w[t, j] dout[t]; dw[t, j] = <dout[t], y[slot_row[t, j]]>."""
     (T, d), k = _dims(dout, 2, "dout"), _dims(slot_row, 2, "slot_row")[1]
-    dev, dt, f32 = _dev(), _dtype(dout, "dout"), torch.float32
+    dev, dt, f32 = _dev(dout), _dtype(dout, "dout"), torch.float32
     _check(load().moe_undispatch_backward(T, k, d, dt, _t(dout, dout.dtype, None, "dout", dev),
                                           _t(y, dout.dtype, (T * k, d), "y", dev),
                                           _t(slot_row, torch.int32, (T, k), "slot_row", dev),
                                           _t(topk_w, f32, (T, k), "topk_w", dev),
                                           _t(dy, dout.dtype, (T * k, d), "dy", dev), _t(dw, f32, (T, k), "dw", dev),
-                                          _stream(stream)), "moe_undispatch_backward")
+                                          _on(stream, dev)), "moe_undispatch_backward")
 
 
 def moe_quantize_fp4(x, codes, scales, stream=None):
     """x [G, rows, K] (bf16, fp16 or fp32) to MXFP4."""
     G, rows, K = _dims(x, 3, "x")
-    dev, dt = _dev(), _dtype(x, "x")
+    dev, dt = _dev(x), _dtype(x, "x")
     _check(load().moe_quantize_fp4(G, rows, K, dt, _t(x, x.dtype, None, "x", dev),
-                                   _f4((codes, scales), G, rows, K, "q", dev), _stream(stream)), "moe_quantize_fp4")
+                                   _f4((codes, scales), G, rows, K, "q", dev), _on(stream, dev)), "moe_quantize_fp4")
 
 
 def moe_dequantize_fp4(codes, scales, x, stream=None):
     """MXFP4 back to x [G, rows, K] (bf16, fp16 or fp32)."""
     G, rows, K = _dims(x, 3, "x")
-    dev, dt = _dev(), _dtype(x, "x")
+    dev, dt = _dev(x), _dtype(x, "x")
     _check(load().moe_dequantize_fp4(G, rows, K, dt, _f4((codes, scales), G, rows, K, "q", dev),
-                                     _t(x, x.dtype, None, "x", dev), _stream(stream)), "moe_dequantize_fp4")
+                                     _t(x, x.dtype, None, "x", dev), _on(stream, dev)), "moe_dequantize_fp4")
 
 
 def moe_dispatch_fp4(x, slot_row, x_sorted, stream=None):
     """moe_dispatch of x's MXFP4 form: x_sorted is an MXFP4 tensor (G = 1) of T * k rows."""
     (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
-    dev, dt = _dev(), _dtype(x, "x")
+    dev, dt = _dev(x), _dtype(x, "x")
     _fp4_dims(x_sorted, "x_sorted")
     _check(load().moe_dispatch_fp4(T, k, d, dt, _t(x, x.dtype, None, "x", dev),
                                    _t(slot_row, torch.int32, (T, k), "slot_row", dev),
-                                   _f4(x_sorted, 1, T * k, d, "x_sorted", dev), _stream(stream)), "moe_dispatch_fp4")
+                                   _f4(x_sorted, 1, T * k, d, "x_sorted", dev), _on(stream, dev)), "moe_dispatch_fp4")
 
 
 def moe_matmul_fp4(a, offsets, W, out, workspace, stream=None):
     """out[r] = a[r] W[e]^T for the rows offsets[e] <= r < offsets[e+1] of every expert e."""
     (_, rows, K), (E, N, _) = _fp4_dims(a, "a"), _fp4_dims(W, "W")
     _dims(out, 2, "out")
-    dev, dt = _dev(), _dtype(out, "out")
+    dev, dt = _dev(out), _dtype(out, "out")
     _check(load().moe_matmul_fp4(rows, E, N, K, _f4(a, 1, rows, K, "a", dev),
                                  _t(offsets, torch.int32, (E + 1,), "offsets", dev), _f4(W, E, N, K, "W", dev), dt,
                                  _t(out, out.dtype, (rows, N), "out", dev),
                                  _t(workspace, torch.uint8, None, "workspace", dev), workspace.numel(),
-                                 _stream(stream)), "moe_matmul_fp4")
+                                 _on(stream, dev)), "moe_matmul_fp4")
 
 
 def moe_swiglu_fp4(a, offsets, W_gate, W_up, h, workspace, stream=None):
@@ -602,12 +610,12 @@ def moe_swiglu_fp4(a, offsets, W_gate, W_up, h, workspace, stream=None):
     (_, rows, K), (E, f, _) = _fp4_dims(a, "a"), _fp4_dims(W_gate, "W_gate")
     _fp4_dims(W_up, "W_up")
     _fp4_dims(h, "h")
-    dev = _dev()
+    dev = _dev(a[0])
     _check(load().moe_swiglu_fp4(rows, E, f, K, _f4(a, 1, rows, K, "a", dev),
                                  _t(offsets, torch.int32, (E + 1,), "offsets", dev),
                                  _f4(W_gate, E, f, K, "W_gate", dev), _f4(W_up, E, f, K, "W_up", dev),
                                  _f4(h, 1, rows, f, "h", dev), _t(workspace, torch.uint8, None, "workspace", dev),
-                                 workspace.numel(), _stream(stream)), "moe_swiglu_fp4")
+                                 workspace.numel(), _on(stream, dev)), "moe_swiglu_fp4")
 
 
 def workspace_view(workspace, shape, region, dtype, dims):

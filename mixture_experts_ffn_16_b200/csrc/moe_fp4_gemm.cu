@@ -311,7 +311,11 @@ __device__ __forceinline__ void emit_h16(const Params& p, const Unit& un, int fe
     const int tok = 8 * o + (lane & 7), stok = 8 * o + (lane >> 2);
     if (c + tok < un.rows)
       *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(tok) * (p.N >> 1) + 4 * (lane >> 3)) = w[o];
-    if ((lane & 3) == 0 && c + stok < un.rows) scales[4 * stok] = static_cast<uint8_t>(byte[o]);
+    if ((lane & 3) == 0 && c + stok < un.rows) {
+      scales[4 * stok] = static_cast<uint8_t>(byte[o]);
+      // f a multiple of 64 only: the last word's two spare bytes
+      if (feat0 + 32 == p.N && (p.N & 127)) *reinterpret_cast<uint16_t*>(scales + 4 * stok + 1) = 0;
+    }
   }
 }
 

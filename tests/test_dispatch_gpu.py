@@ -176,3 +176,69 @@ def test_rows_out_of_range_count_as_none():
     dy, dw = torch.zeros_like(xs), torch.empty(T, k, device="cuda")
     api.moe_undispatch_backward(x, xs, slot_row, w, dy, dw)
     assert torch.equal(dy, xs) and (dw[2] == 0).all() and dw[0, 1] == 0 and dw[1, 0] == 0
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements of sorted rows."""
+    T, k, d = 4100, 8, 65536
+    offsets, slot_row = ref.sort_tokens(np.random.default_rng(1).permuted(np.tile(np.arange(8, dtype=np.int32), (T, 1)),
+                                                                          axis=1), 8)
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    xs = torch.empty(T * k, d, dtype=torch.bfloat16, device="cuda")
+    rows = dev(slot_row)
+    api.moe_dispatch(x, rows, xs)
+    for j in range(k):
+        for t0 in range(0, T, 1025):
+            assert torch.equal(xs[rows[t0:t0 + 1025, j].long()], x[t0:t0 + 1025])
+    w = torch.full((T, k), 0.125, device="cuda")
+    out = torch.empty_like(x)
+    api.moe_undispatch(xs, rows, w, out)                 # eight equal rows, weights that add up to 1: exact
+    assert torch.equal(out, x)
+    dy, dw = torch.zeros_like(xs), torch.empty(T, k, device="cuda")
+    api.moe_undispatch_backward(x, xs, rows, w, dy, dw)
+    assert torch.equal(dy[rows[4099, 7].long()], (x[4099].float() * 0.125).bfloat16())
+    assert torch.equal(dy[T * k - 1], (xs[T * k - 1].float() * 0.125).bfloat16())
+    want = x[4099].double().square().sum().item()
+    assert abs(dw[4099, 3].item() - want) <= (d / 256 + 24) * 2.0 ** -24 * want
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_against_differences(dtype):
+    """The loss sum(out * g) of dispatch -> undispatch, differentiated by dispatch_backward and undispatch_backward,
+    against central differences of the loss in doubles (the loss is linear in x and in the weights: exact up to
+    the kernels' own rounding)."""
+    T, k, d, E = 7, 3, 64, 4
+    rng = np.random.default_rng(12)
+    offsets, slot_row = ref.sort_tokens(ref.routing(rng, T, k, E, drop=0.2), E)
+    rows = dev(slot_row)
+    x = torch.from_numpy(rng.standard_normal((T, d))).to(dtype).cuda()
+    w = torch.from_numpy(rng.random((T, k))).float().cuda()
+    g = torch.from_numpy(rng.standard_normal((T, d))).to(dtype).cuda()
+    xs, dxs = torch.zeros(T * k, d, dtype=dtype, device="cuda"), torch.zeros(T * k, d, dtype=dtype, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    api.moe_dispatch(x, rows, xs)
+    api.moe_undispatch_backward(g, xs, rows, w, dxs, dw)
+    api.moe_dispatch_backward(dxs, rows, dx)
+
+    xv, wv, gv = (t.double().cpu().numpy() for t in (x, w, g))
+    has = slot_row >= 0
+
+    def loss(xv, wv):
+        return float(((has * wv).sum(1)[:, None] * xv * gv).sum())
+
+    half = torch.finfo(dtype).eps / 2
+    for t in range(T):
+        for j in range(k):
+            e = np.zeros_like(wv)
+            e[t, j] = 0.5
+            want = loss(xv, wv + e) - loss(xv, wv - e)
+            size = np.abs(xv[t] * gv[t]).sum()
+            # 64 products and sums in fp32; the differences lose 2^-52 of the whole loss
+            assert abs(dw[t, j].item() - want) <= 24 * 2.0 ** -24 * size + 1e-12
+        for i in range(0, d, 7):
+            e = np.zeros_like(xv)
+            e[t, i] = 0.5
+            want = loss(xv + e, wv) - loss(xv - e, wv)
+            size = np.abs(has[t] * wv[t] * gv[t, i]).sum()
+            # each of k terms rounded to the type, k additions, one more rounding
+            assert abs(dx[t, i].item() - want) <= (2 * half + (k + 1) * 2.0 ** -24) * 1.01 * size + 1e-12

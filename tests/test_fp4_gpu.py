@@ -7,6 +7,7 @@ import torch
 
 import fp4_ref as ref
 from mixture_experts_ffn_16_b200 import api
+from mixture_experts_ffn_16_b200.inputs import MoEConfig, make_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -154,7 +155,7 @@ def check_swiglu(got_codes, got_scales, g, u, size_g, size_u, K):
     """Kernel h (codes, scale bytes [rows, f/32]) against doubles g, u."""
     # accumulator errors of both products, and a few fp32 ulps for the sigmoid
     dg, du = (K / 64) * 2.0 ** -22 * size_g, (K / 64) * 2.0 ** -22 * size_u
-    s = 1.0 / (1.0 + np.exp(-g))
+    s = np.exp(-np.logaddexp(0.0, -g))
     h = g * s * u
     slope = np.abs(s * (1.0 + g * (1.0 - s)))
     delta = (slope + 1e-3) * dg * (np.abs(u) + du) + np.abs(g * s) * du + 2.0 ** -19 * (1 + np.abs(g)) * np.abs(h)
@@ -179,6 +180,7 @@ def test_swiglu(counts, behind, f, K):
     off = offsets_of(counts)
     E, rows = len(counts), int(off[-1]) + behind
     a, av = random_fp4(rng, 1, rows, K, spread=1)
+    a[0][0, 0], av[0, 0] = 0, 0.0                        # a row of zeros
     # weights that keep g around 1
     wg, wgv = random_fp4(rng, E, f, K, spread=1)
     wu, wuv = random_fp4(rng, E, f, K, spread=1)
@@ -198,3 +200,229 @@ def test_swiglu(counts, behind, f, K):
             check_swiglu(codes[r], scales[r], x @ wgv[e].T, x @ wuv[e].T, np.abs(x) @ np.abs(wgv[e]).T,
                          np.abs(x) @ np.abs(wuv[e]).T, K)
     assert (h[0][0, off[-1]:] == 0xEE).all() and (h[1][0, :, off[-1]:] == 0xEE).all()
+    if f % 128:                                          # the spare bytes of the last word
+        assert not h[1][0, -1, :off[-1], 2:].any()
+
+
+# ---------------------------------------------------------------- special values, bounds, streams, graphs
+
+def test_nan_scales_stay_in_their_rows_and_columns():
+    """A NaN block of an activation row makes that row NaN, one of a weight row that output column; nothing else."""
+    rng = np.random.default_rng(3)
+    for counts in ([5, 9], [150, 120]):                  # single CTAs, CTA pairs
+        off = offsets_of(counts)
+        rows, N, K = int(off[-1]), 192, 256
+        a, av = random_fp4(rng, 1, rows, K)
+        w, wv = random_fp4(rng, 2, N, K)
+        a[1][0, 1, 3, 2] = 255                           # row 3, elements 192..223
+        w[1][1, 0, 70, 1] = 255                          # expert 1, output 70
+        out = torch.empty(rows, N, device="cuda")
+        ws = api.alloc_dispatch_workspace()
+        api.moe_matmul_fp4(a, dev(off), w, out, ws)
+        got = out.cpu().numpy()
+        want = np.zeros((rows, N), dtype=bool)
+        want[3], want[off[1]:, 70] = True, True
+        assert np.array_equal(np.isnan(got), want)
+        # through the gate/up product: the whole row, and the block of 32 the column lies in
+        wu, _ = random_fp4(rng, 2, N, K)
+        h = api.fp4_empty(1, rows, N)
+        api.moe_swiglu_fp4(a, dev(off), w, wu, h, ws)
+        nan = ref.rows_of_scales(h[1].cpu().numpy(), N)[0] == 255
+        expect = np.zeros((rows, N // 32), dtype=bool)
+        expect[3], expect[off[1]:, 70 // 32] = True, True
+        assert np.array_equal(nan, expect)
+        codes = ref.unpack(h[0].cpu().numpy())[0]
+        assert not codes[nan.repeat(32, -1)].any()
+
+
+@pytest.mark.parametrize("off", [[0, 90, 40, 200], [-7, 3, 10 ** 9, 5], [200, 100, 50, 0], [300, 300, 300, 300]])
+def test_invalid_offsets_stay_in_bounds(off):
+    """Offsets that decrease or leave [0, rows]: clamped, and no row outside the tensor is touched."""
+    rng = np.random.default_rng(4)
+    rows, N, K = 130, 128, 192
+    a, _ = random_fp4(rng, 1, rows, K)
+    w, _ = random_fp4(rng, 3, N, K)
+    guarded = torch.full((rows + 64, N), 5.0, device="cuda")
+    ws = api.alloc_dispatch_workspace()
+    api.moe_matmul_fp4(a, dev(np.array(off, dtype=np.int32)), w, guarded[32:32 + rows], ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    assert bool((guarded[:32] == 5).all()) and bool((guarded[32 + rows:] == 5).all())
+
+
+def test_products_past_32_bit_offsets():
+    """Outputs of more than 2^31 elements, in the last rows; K a multiple of 64 only."""
+    rng = np.random.default_rng(6)
+    rows, N, K = 33003, 65536, 192
+    off = offsets_of([3, 32990])
+    a, av = random_fp4(rng, 1, rows, K)
+    w, wv = random_fp4(rng, 2, N, K)
+    out = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    ws = api.alloc_dispatch_workspace()
+    api.moe_matmul_fp4(a, dev(off), w, out, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    for r in (0, 3, 20000, 32980, 32992):
+        want = wv[0 if r < 3 else 1] @ av[0, r]
+        size = np.abs(wv[0 if r < 3 else 1]) @ np.abs(av[0, r])
+        add = (K / 64) * 2.0 ** -22 * size
+        assert ref.within(out[r].double().cpu().numpy(), want, add + ref.half_step(out.dtype, np.abs(want) + add))
+    assert not bool(out[32993:].any())
+    del out
+    h = api.fp4_empty(1, rows, N)                        # 2^31 codes, and the scales behind them
+    h[1].zero_()
+    api.moe_swiglu_fp4(a, dev(off), w, w, h, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    r = 32992
+    codes = ref.unpack(h[0][:, r:r + 1].cpu().numpy())[0]
+    scales = ref.rows_of_scales(h[1][:, :, r:r + 1].cpu().numpy(), N)[0]
+    x, big = av[0, r:r + 1], np.abs(av[0, r:r + 1]) @ np.abs(wv[1]).T
+    check_swiglu(codes, scales, x @ wv[1].T, x @ wv[1].T, big, big, K)
+
+
+class Chain:
+    """One layer's experts from the routing to the tokens: route, sort, dispatch_fp4, swiglu, matmul, undispatch."""
+
+    def __init__(self, T, d, f, E, k, seed):
+        self.cfg = MoEConfig("fp4_chain", T=T, d=d, E=E, k=k, f=f, S=0, fs=0, score_fn="softmax", seed=seed)
+        self.inp = make_inputs(self.cfg, device="cuda")
+        self.shape = api.shape_of(self.cfg)
+        self.route_ws = api.alloc_workspace(self.shape)
+        self.ws = api.alloc_dispatch_workspace()
+        q = {}
+        for name in ("W_gate", "W_up", "W_down"):
+            q[name] = api.fp4_empty(E, *self.inp[name].shape[1:])
+            api.moe_quantize_fp4(self.inp[name], *q[name])
+        self.q = q
+        self.x = self.inp["x"].clone()
+        self.idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+        self.w = torch.empty(T, k, device="cuda")
+        self.offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+        self.slot_row = torch.empty(T, k, dtype=torch.int32, device="cuda")
+        self.a, self.h = api.fp4_empty(1, T * k, d), api.fp4_empty(1, T * k, f)
+        self.y = torch.empty(T * k, d, dtype=torch.bfloat16, device="cuda")
+        self.out = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+
+    def __call__(self, stream=None):
+        c = self.cfg
+        api.moe_route(self.shape, self.x, self.inp["W_router"], None, c.score_fn, True, 1.0, self.idx, self.w,
+                      self.route_ws, stream)
+        api.moe_sort_tokens(self.idx, self.offsets, self.slot_row, self.ws, stream)
+        api.moe_dispatch_fp4(self.x, self.slot_row, self.a, stream)
+        api.moe_swiglu_fp4(self.a, self.offsets, self.q["W_gate"], self.q["W_up"], self.h, self.ws, stream)
+        api.moe_matmul_fp4(self.h, self.offsets, self.q["W_down"], self.y, self.ws, stream)
+        api.moe_undispatch(self.y, self.slot_row, self.w, self.out, stream)
+        return self.out
+
+    def state(self):
+        return [t.clone() for t in (self.idx, self.w, self.offsets, self.slot_row, *self.a, *self.h, self.y, self.out)]
+
+
+@pytest.mark.parametrize("T,d,f,E,k", [(1, 128, 64, 8, 2), (70, 256, 192, 12, 3), (500, 512, 256, 6, 2)])
+def test_chain_of_an_expert_layer(T, d, f, E, k):
+    """Each step checked in doubles from what the step before it left."""
+    c = Chain(T, d, f, E, k, seed=T)
+    c()
+    assert api.moe_device_status(c.ws) == api.MOE_OK
+    idx, slot_row = c.idx.cpu().numpy(), c.slot_row.cpu().numpy()
+    off, rows = ref.sort_tokens(idx, E)
+    assert np.array_equal(c.offsets.cpu().numpy(), off) and np.array_equal(slot_row, rows)
+    a = ref.dequantize(*(t.cpu().numpy() for t in c.a))[0]
+    xq = ref.dequantize(*ref.pack(*(t[None] for t in ref.quantize(c.x.double().cpu().numpy()))))[0]
+    tok = np.empty(T * k, dtype=int)
+    tok[rows.reshape(-1)] = np.arange(T * k) // k
+    assert np.array_equal(a, xq[tok])
+    W = {n: ref.dequantize(*(t.cpu().numpy() for t in c.q[n])) for n in c.q}
+    hc, hs = ref.unpack(c.h[0].cpu().numpy())[0], ref.rows_of_scales(c.h[1].cpu().numpy(), f)[0]
+    h = ref.dequantize(*(t.cpu().numpy() for t in c.h))[0]
+    y = c.y.double().cpu().numpy()
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        if r.start == r.stop:
+            continue
+        check_swiglu(hc[r], hs[r], a[r] @ W["W_gate"][e].T, a[r] @ W["W_up"][e].T,
+                     np.abs(a[r]) @ np.abs(W["W_gate"][e]).T, np.abs(a[r]) @ np.abs(W["W_up"][e]).T, d)
+        want, size = h[r] @ W["W_down"][e].T, np.abs(h[r]) @ np.abs(W["W_down"][e]).T
+        add = (f / 64 + 1) * 2.0 ** -22 * size
+        assert ref.within(y[r], want, add + ref.half_step(c.y.dtype, np.abs(want) + add))
+    w = c.w.double().cpu().numpy()
+    terms = w[..., None] * y[rows]
+    want, add = terms.sum(1), k * 2.0 ** -24 * np.abs(terms).sum(1)
+    assert ref.within(c.out.double().cpu().numpy(), want, add + ref.half_step(c.out.dtype, np.abs(want) + add))
+
+
+def test_chain_repeats_bitwise_on_another_stream_and_from_a_graph():
+    """The same bits from the current stream, a side stream, and a captured graph replayed on other inputs."""
+    c = Chain(300, 256, 192, 5, 2, seed=9)
+    c()
+    first = c.state()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for t in (c.idx, c.offsets, c.slot_row, *c.a, *c.h, c.y, c.out):
+        t.fill_(1)
+    side.wait_stream(torch.cuda.current_stream())
+    c(side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(p, q) for p, q in zip(first, c.state()))
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c()
+    other = torch.randn_like(c.x)
+    c.x.copy_(other)
+    c()
+    want = c.state()
+    assert not torch.equal(want[-1], first[-1])
+    c.x.copy_(c.inp["x"])
+    graph.replay()
+    assert all(torch.equal(p, q) for p, q in zip(first, c.state()))
+    c.x.copy_(other)
+    graph.replay()
+    graph.replay()
+    assert all(torch.equal(p, q) for p, q in zip(want, c.state()))
+    assert api.moe_device_status(c.ws) == api.MOE_OK
+
+
+def test_two_layers_on_two_streams_at_once():
+    """Two chains, each with its own workspace, interleaved on two streams."""
+    chains = [Chain(400, 512, 256, 4, 2, seed=21), Chain(37, 256, 128, 16, 4, seed=22)]
+    want = []
+    for c in chains:
+        c()
+        want.append(c.state())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(chains, streams):
+            c(s)
+    torch.cuda.synchronize()
+    for c, w in zip(chains, want):
+        assert all(torch.equal(p, q) for p, q in zip(w, c.state()))
+        assert api.moe_device_status(c.ws) == api.MOE_OK
+
+
+def test_refusals_on_the_device():
+    rng = np.random.default_rng(8)
+    a, _ = random_fp4(rng, 1, 8, 128)
+    w, _ = random_fp4(rng, 2, 64, 128)
+    off, ws = dev(offsets_of([3, 5])), api.alloc_dispatch_workspace()
+    out = torch.full((8, 64), 3.0, device="cuda")
+    with pytest.raises(ValueError, match="out"):
+        api.moe_matmul_fp4(a, off, w, torch.empty(9, 64, device="cuda"), ws)
+    with pytest.raises(ValueError, match="offsets"):
+        api.moe_matmul_fp4(a, off[:2], w, out, ws)
+    with pytest.raises(ValueError, match="a.scales"):
+        api.moe_matmul_fp4((a[0], a[1][:, :, :7]), off, w, out, ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        api.moe_matmul_fp4(a, off, w, torch.empty(64, 8, device="cuda").t(), ws)
+    with pytest.raises(TypeError, match="out"):
+        api.moe_matmul_fp4(a, off, w, torch.empty(8, 64, dtype=torch.float64, device="cuda"), ws)
+    with pytest.raises(ValueError, match="offsets"):
+        api.moe_matmul_fp4(a, off.cpu(), w, out, ws)
+    with pytest.raises(api.MoEError) as e:
+        api.moe_matmul_fp4(a, off, w, out, ws[:128])
+    assert e.value.status == api.MOE_ERR_WORKSPACE
+    with pytest.raises(api.MoEError) as e:                      # K = 32
+        api.moe_quantize_fp4(torch.zeros(1, 2, 32, device="cuda"), *api.fp4_empty(1, 2, 32))
+    assert e.value.status == api.MOE_ERR_UNSUPPORTED
+    torch.cuda.synchronize()
+    assert bool((out == 3.0).all())
