@@ -22,12 +22,12 @@ namespace {
 
 // ---------------------------------------------------------------- sort
 
-constexpr int kSortWarps = 16;
-constexpr int kSortThreads = 32 * kSortWarps;
 constexpr int kSortMaxCluster = 8;                       // the portable cluster size
-constexpr int kSortPer = kMaxE / kSortThreads;           // experts per thread
-constexpr int kSortBits = 12;                            // of the numbers 0..kMaxE
 constexpr int kSortBatch = 8;                            // groups of 32 slots a warp has in flight
+
+// Warps of a CTA: 16 up to 1024 experts, above that 8, whose counters and lane
+// masks (one of each per warp and expert) still fit in shared memory.
+constexpr int sort_experts(int warps) { return warps == 16 ? 1024 : kMaxE; }
 
 __device__ __forceinline__ uint32_t cluster_nctas() {
   uint32_t r;
@@ -41,29 +41,38 @@ __device__ __forceinline__ int ld_cluster(uint32_t cluster_addr) {
   return v;
 }
 
-// One cluster sorts all slots.  Warp w of CTA c owns the c * kSortWarps + w-th
+// One cluster sorts all slots.  Warp w of CTA c owns the c * WARPS + w-th
 // run of consecutive slots.  Pass 1 counts each warp's slots per expert in
 // shared memory; prefix sums over warps, then (through distributed shared
 // memory) over CTAs, then over experts give each (warp, expert) its first
 // row; pass 2 walks the slots again and places them, 32 at a time, each
-// behind the lower lanes with the same expert: the order of slots inside an
-// expert is kept.  One launch instead of the count / scan / scatter of three.
-__global__ void __launch_bounds__(kSortThreads)
+// behind the lower lanes with the same expert (each lane sets its bit in the
+// expert's mask): the order of slots inside an expert is kept.  One launch
+// instead of the count / scan / scatter of three.  Bound by the instructions
+// of pass 2 on the cluster's SMs; 65k slots of 256 experts took 15.1 us with a
+// warp match for the lanes of one expert, 11.0 us with a vote per bit.
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS)
 sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t* __restrict__ offsets,
             int32_t* __restrict__ slot_row, uint32_t* __restrict__ err) {
+  constexpr int kThreads = 32 * WARPS, kPer = sort_experts(WARPS) / kThreads;   // kPer: experts per thread
   extern __shared__ int32_t sm[];
-  int32_t* hist = sm;                       // [kSortWarps][E]
-  int32_t* total = sm + kSortWarps * E;     // [E] this CTA's counts
-  __shared__ int32_t wsum[kSortWarps];
+  int32_t* hist = sm;                       // [WARPS][E]
+  int32_t* total = sm + WARPS * E;          // [E] this CTA's counts
+  uint32_t* masks = reinterpret_cast<uint32_t*>(total + E);   // [WARPS][E]
+  __shared__ int32_t wsum[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank(), ctas = cluster_nctas();
-  for (int i = tid; i < kSortWarps * E; i += kSortThreads) hist[i] = 0;
+  for (int i = tid; i < WARPS * E; i += kThreads) {
+    hist[i] = 0;
+    masks[i] = 0;
+  }
   chain_wait();
   if (rank == 0 && tid == 0) *err = 0;
   __syncthreads();
 
   int32_t* mine = hist + warp * E;
-  const int64_t lo = static_cast<int64_t>(rank * kSortWarps + warp) * run;
+  const int64_t lo = static_cast<int64_t>(rank * WARPS + warp) * run;
   const int begin = static_cast<int>(min(lo, static_cast<int64_t>(n)));
   const int end = static_cast<int>(min(lo + run, static_cast<int64_t>(n)));
   // The loads of a batch are issued before any is used.
@@ -82,10 +91,10 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
       if (e[q] >= 0 && e[q] < E) atomicAdd(mine + e[q], 1);
   }
   __syncthreads();
-  for (int e = tid; e < E; e += kSortThreads) {
+  for (int e = tid; e < E; e += kThreads) {
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const int c = hist[w * E + e];
       hist[w * E + e] = s;
       s += c;
@@ -95,11 +104,11 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   cluster_sync();
 
   // thread t: experts t * per .. + per - 1
-  const int per = (E + kSortThreads - 1) / kSortThreads;
-  int below[kSortPer], all[kSortPer];
+  const int per = (E + kThreads - 1) / kThreads;
+  int below[kPer], all[kPer];
   int sum = 0;
 #pragma unroll
-  for (int q = 0; q < kSortPer; ++q) {
+  for (int q = 0; q < kPer; ++q) {
     below[q] = all[q] = 0;
     const int e = tid * per + q;
     if (q < per && e < E) {
@@ -123,11 +132,11 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   int base = inc - sum;
   for (int w = 0; w < warp; ++w) base += wsum[w];
 #pragma unroll
-  for (int q = 0; q < kSortPer; ++q) {
+  for (int q = 0; q < kPer; ++q) {
     const int e = tid * per + q;
     if (q < per && e < E) {
       if (rank == 0) offsets[e] = base;
-      total[e] = base + below[q];
+      for (int w = 0; w < WARPS; ++w) hist[w * E + e] += base + below[q];     // first row of each warp's
       base += all[q];
       if (rank == 0 && e == E - 1) offsets[E] = base;
     }
@@ -136,41 +145,30 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
 
   uint32_t lt;
   asm volatile("mov.u32 %0, %%lanemask_lt;" : "=r"(lt));
-  const int bits = 32 - __clz(E);           // of the numbers 0..E, E standing for no expert
+  uint32_t* mask = masks + warp * E;
   bool bad = false;
   for (int i0 = begin; i0 < end; i0 += 32 * kSortBatch) {
     int e[kSortBatch];
     load(e, i0);
-    // The lanes with the same expert, by one vote per bit of its number: a warp
-    // match takes a step for each distinct value (65k slots of 256 experts:
-    // 15.1 us with it).
-    uint32_t peers[kSortBatch];
-#pragma unroll
-    for (int q = 0; q < kSortBatch; ++q) {
-      bad |= e[q] < -1 || e[q] >= E;
-      if (e[q] < 0 || e[q] >= E) e[q] = E;
-      peers[q] = 0xffffffffu;
-    }
-#pragma unroll
-    for (int b = 0; b < kSortBits; ++b) {
-      if (b < bits) {
-#pragma unroll
-        for (int q = 0; q < kSortBatch; ++q) {
-          const bool one = (e[q] >> b) & 1;
-          const uint32_t v = __ballot_sync(0xffffffffu, one);
-          peers[q] &= one ? v : ~v;
-        }
-      }
-    }
 #pragma unroll
     for (int q = 0; q < kSortBatch; ++q) {
       if (i0 + 32 * q >= end) break;
       const int x = e[q];
-      const int rank_in = __popc(peers[q] & lt);
-      int row = -1;
-      if (x < E) row = total[x] + mine[x] + rank_in;
+      const bool has = x >= 0 && x < E;
+      bad |= !has && x != -1;
+      if (has) atomicOr(mask + x, 1u << lane);
       __syncwarp();
-      if (x < E && rank_in == 0) mine[x] += __popc(peers[q]);
+      int row = -1;
+      uint32_t peers = 0;
+      if (has) {
+        peers = mask[x];
+        row = mine[x] + __popc(peers & lt);
+      }
+      __syncwarp();
+      if (has && (peers & lt) == 0) {        // the first of them
+        mask[x] = 0;
+        mine[x] += __popc(peers);
+      }
       __syncwarp();
       const int i = i0 + 32 * q + lane;
       if (i < end) slot_row[i] = row;
@@ -409,19 +407,18 @@ int undispatch_backward_t(int tokens, int k, int d, const void* dout, const void
 
 }  // namespace
 
-int launch_sort_tokens(int T, int k, int E, const int32_t* topk_idx, int32_t* offsets, int32_t* slot_row,
-                       uint32_t* err, cudaStream_t st) {
-  const int n = T * k;
-  // CTAs: enough that a warp walks at most 8 groups of 32 slots, up to the
-  // portable cluster size.
+template <int WARPS>
+static int launch_sort(int n, int E, const int32_t* topk_idx, int32_t* offsets, int32_t* slot_row, uint32_t* err,
+                       cudaStream_t st) {
+  // CTAs: enough that a warp walks one batch of slots, up to the portable
+  // cluster size.
   int ctas = 1;
-  while (ctas < kSortMaxCluster && static_cast<int64_t>(ctas) * kSortThreads * 8 < n) ctas *= 2;
-  const int warps = ctas * kSortWarps;
+  while (ctas < kSortMaxCluster && static_cast<int64_t>(ctas) * 32 * WARPS * kSortBatch < n) ctas *= 2;
+  const int warps = ctas * WARPS;
   const int run = static_cast<int>((static_cast<int64_t>(n) + warps * 32 - 1) / (warps * 32)) * 32;
-  const size_t smem = static_cast<size_t>(kSortWarps + 1) * E * sizeof(int32_t);
   static std::atomic<int> limit[64];
-  const int rc = raise_smem_limit(sort_kernel, limit,
-                                  (kSortWarps + 1) * kMaxE * static_cast<int>(sizeof(int32_t)));
+  const int rc = raise_smem_limit(sort_kernel<WARPS>, limit,
+                                  (2 * WARPS + 1) * sort_experts(WARPS) * static_cast<int>(sizeof(int32_t)));
   if (rc != MOE_OK) return rc;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -432,12 +429,18 @@ int launch_sort_tokens(int T, int k, int E, const int32_t* topk_idx, int32_t* of
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(32 * WARPS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(2 * WARPS + 1) * E * sizeof(int32_t);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return ok_or_cuda(cudaLaunchKernelEx(&cfg, sort_kernel, topk_idx, n, E, run, offsets, slot_row, err));
+  return ok_or_cuda(cudaLaunchKernelEx(&cfg, sort_kernel<WARPS>, topk_idx, n, E, run, offsets, slot_row, err));
+}
+
+int launch_sort_tokens(int T, int k, int E, const int32_t* topk_idx, int32_t* offsets, int32_t* slot_row,
+                       uint32_t* err, cudaStream_t st) {
+  return E <= sort_experts(16) ? launch_sort<16>(T * k, E, topk_idx, offsets, slot_row, err, st)
+                               : launch_sort<8>(T * k, E, topk_idx, offsets, slot_row, err, st);
 }
 
 int launch_dispatch(int T, int k, size_t row_bytes, const void* x, const int32_t* slot_row, void* x_sorted,
