@@ -159,17 +159,20 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
 }
 
 // Rows of K elements as a flat sequence of groups of 8, each row padded to P
-// groups.  Division by P by multiplication: m64 = ceil(2^64 / P) is exact for
-// the first group of a warp (below 2^41, P at most 2^13), m32 = ceil(2^32 / P)
-// for offsets below P + 128.
+// groups.  Divisions by multiplication: by P with m64 = ceil(2^64 / P), exact
+// for the first group of a warp (below 2^41, P at most 2^13), and with m32 =
+// ceil(2^32 / P) for offsets below P + 128; by the rows of a matrix with g64 =
+// ceil(2^64 / per_matrix) for rows below 2^28 (0 stands for 2^64, one matrix
+// a row).
 struct Layout {
   int64_t rows;
-  uint64_t m64;
+  uint64_t m64, g64;
   uint32_t m32;
   int P, groups, chunks, per_matrix;     // groups = K / 8; rows per matrix
 };
 
-// The groups of one warp: they start at group rem0 of row row0.
+// The groups of one warp: they start at group rem0 of row row0.  WHOLE: K is a
+// multiple of 1024, so the warp's 128 groups lie in one row and all exist.
 struct Span {
   int64_t row0;
   uint32_t rem0;
@@ -185,23 +188,29 @@ __device__ __forceinline__ Span warp_span(const Layout& l) {
   return s;
 }
 // Group `o` of the warp's: its row, counted from row0, and its place in the
-// row; false behind the last row.
+// row; false behind the row's end or the last row.
+template <bool WHOLE>
 __device__ __forceinline__ bool locate(const Layout& l, const Span& s, int o, int* dr, int* u) {
+  if constexpr (WHOLE) {
+    *dr = 0;
+    *u = static_cast<int>(s.rem0) + o;
+    return s.left > 0;
+  }
   const uint32_t t = s.rem0 + static_cast<uint32_t>(o);
   *dr = static_cast<int>(__umulhi(t, l.m32));
   *u = static_cast<int>(t) - *dr * l.P;
-  return *dr < s.left;
+  return *dr < s.left && *u < l.groups;
 }
 // Word index of chunk c of row r in the scales.
 __device__ __forceinline__ int64_t scale_at(const Layout& l, int64_t row, int chunk) {
   if (l.rows == l.per_matrix) return chunk * l.rows + row;
-  const int64_t g = row / l.per_matrix;
+  const int64_t g = l.g64 ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(row), l.g64)) : row;
   return (g * l.chunks + chunk) * l.per_matrix + (row - g * l.per_matrix);
 }
 
 // SLOTS: row = token; the codes and scales go to the rows that its k slots
 // have (slot_row), the token being read and quantised once.
-template <typename T, bool SLOTS>
+template <typename T, bool SLOTS, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __restrict__ scales,
                 const __grid_constant__ Layout l, const int32_t* __restrict__ slot_row, int k) {
@@ -213,7 +222,7 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
     int dr, u;
-    if (locate(l, s, 32 * j + lane, &dr, &u) && u < l.groups)
+    if (locate<WHOLE>(l, s, 32 * j + lane, &dr, &u))
       f[j].load(x0 + (dr * l.groups + u) * 8);
     else
       f[j].zero();
@@ -230,8 +239,8 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
   transpose4(w);
   const uint4 block = make_uint4(w[0], w[1], w[2], w[3]);
   int bdr, bu, sdr, su;
-  const bool bin = locate(l, s, 32 * (lane & 3) + (lane & ~3), &bdr, &bu) && bu < l.groups;   // this lane's block of 32
-  const bool sin = locate(l, s, 16 * (lane & 7), &sdr, &su) && lane < 8;                      // lanes 0..7: chunk of 128
+  const bool bin = locate<WHOLE>(l, s, 32 * (lane & 3) + (lane & ~3), &bdr, &bu);   // this lane's block of 32
+  const bool sin = locate<WHOLE>(l, s, 16 * (lane & 7), &sdr, &su) && lane < 8;             // lanes 0..7: chunk of 128
   const int64_t brow = s.row0 + bdr, srow = s.row0 + sdr;
   if constexpr (SLOTS) {
     const uint32_t R = static_cast<uint32_t>(l.rows) * static_cast<uint32_t>(k);
@@ -239,6 +248,18 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
     const int32_t* sto = slot_row + srow * k;
     uint4* const c0 = codes + (bu >> 2);
     uint32_t* const s0 = scales + static_cast<size_t>(su >> 4) * R;
+    if constexpr (WHOLE) {
+      // one token a warp: a lane a slot
+      const uint32_t mine = (lane < k && s.left > 0) ? static_cast<uint32_t>(__ldg(bto + lane)) : R;
+#pragma unroll 4
+      for (int j = 0; j < k; ++j) {
+        const uint32_t r = __shfl_sync(0xffffffffu, mine, j);
+        if (r >= R) continue;
+        __stcs(c0 + static_cast<size_t>(r) * (l.groups >> 2), block);
+        if (lane < 8) s0[r] = word;
+      }
+      return;
+    }
 #pragma unroll 4
     for (int j = 0; j < k; ++j) {
       if (bin) {
@@ -256,7 +277,7 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
   }
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
 dequantize_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ scales, T* __restrict__ x,
                   const __grid_constant__ Layout l) {
@@ -264,7 +285,7 @@ dequantize_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ 
   const int lane = threadIdx.x & 31;
   const Span s = warp_span(l);
   int bdr, bu;                                                  // the block of 32 this lane loads
-  const bool bin = locate(l, s, 32 * (lane & 3) + (lane & ~3), &bdr, &bu) && bu < l.groups;
+  const bool bin = locate<WHOLE>(l, s, 32 * (lane & 3) + (lane & ~3), &bdr, &bu);
   uint32_t w[kUnits] = {0, 0, 0, 0}, byte = 0;
   if (bin) {
     const int64_t brow = s.row0 + bdr;
@@ -279,7 +300,7 @@ dequantize_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ 
     // unit j of this lane lies in the block that lane (lane & ~3) + j loaded
     const float sc = fp4_scale(__shfl_sync(0xffffffffu, byte, (lane & ~3) + j));
     int dr, u;
-    if (locate(l, s, 32 * j + lane, &dr, &u) && u < l.groups) {
+    if (locate<WHOLE>(l, s, 32 * j + lane, &dr, &u)) {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -302,6 +323,7 @@ Layout make_layout(int64_t rows, int per_matrix, int K) {
   l.P = 16 * l.chunks;
   l.m64 = ~0ull / l.P + 1;          // ceil(2^64 / P), P being at least 16 (a power of two: exactly 2^64 / P)
   l.m32 = static_cast<uint32_t>(((1ull << 32) + l.P - 1) / l.P);
+  l.g64 = per_matrix > 1 ? ~0ull / per_matrix + 1 : 0;
   return l;
 }
 dim3 layout_grid(const Layout& l) {
@@ -313,7 +335,8 @@ template <typename T, bool SLOTS>
 int quantize_t(int64_t rows, int per_matrix, int K, const void* x, const int32_t* slot_row, int k, void* codes,
                void* scales, cudaStream_t st) {
   const Layout l = make_layout(rows, per_matrix, K);
-  return launch_chained(quantize_kernel<T, SLOTS>, layout_grid(l), dim3(kThreads), 0, st, static_cast<const T*>(x),
+  const auto kern = K % 1024 ? quantize_kernel<T, SLOTS, false> : quantize_kernel<T, SLOTS, true>;
+  return launch_chained(kern, layout_grid(l), dim3(kThreads), 0, st, static_cast<const T*>(x),
                         static_cast<uint4*>(codes), static_cast<uint32_t*>(scales), l, slot_row, k) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
@@ -323,7 +346,8 @@ template <typename T>
 int dequantize_t(int64_t rows, int per_matrix, int K, const void* codes, const void* scales, void* x,
                  cudaStream_t st) {
   const Layout l = make_layout(rows, per_matrix, K);
-  return launch_chained(dequantize_kernel<T>, layout_grid(l), dim3(kThreads), 0, st,
+  const auto kern = K % 1024 ? dequantize_kernel<T, false> : dequantize_kernel<T, true>;
+  return launch_chained(kern, layout_grid(l), dim3(kThreads), 0, st,
                         static_cast<const uint4*>(codes), static_cast<const uint32_t*>(scales), static_cast<T*>(x),
                         l) == cudaSuccess
              ? MOE_OK

@@ -48,7 +48,7 @@ def hard_rows(rng, rows, K, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("G,rows,K", [(1, 1, 64), (1, 3, 128), (2, 7, 192), (3, 33, 320), (1, 5, 4096), (2, 2, 4160),
-                                      (1, 300, 64), (1, 2, 65536)])
+                                      (1, 300, 64), (1, 2, 65536), (3, 5, 1024)])
 def test_quantize_matches_the_definition(G, rows, K, dtype):
     rng = np.random.default_rng(rows * K)
     x = torch.stack([hard_rows(rng, rows, K, dtype) for _ in range(G)])
@@ -95,7 +95,8 @@ def test_quantize_extremes(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T,d,k,E", [(1, 64, 1, 1), (5, 192, 3, 4), (37, 4096, 8, 20), (3, 8256, 32, 40)])
+@pytest.mark.parametrize("T,d,k,E", [(1, 64, 1, 1), (5, 192, 3, 4), (37, 4096, 8, 20), (3, 8256, 32, 40),
+                                     (6, 1024, 32, 7)])
 def test_dispatch_fp4_is_quantize_then_dispatch(T, d, k, E, dtype):
     rng = np.random.default_rng(T + d)
     idx = ref.routing(rng, T, k, E, drop=0.2)
