@@ -34,17 +34,8 @@ __device__ __forceinline__ float fp4_scale(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : (byte == kFp4NanScale ? 0x7FC00000u : byte << 23));
 }
 
-// Two floats to a byte of two E2M1 codes (round to nearest even, saturating),
-// `lo` in the low half.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-// Eight floats (already divided by their scale) to eight codes, the first in
-// the lowest bits.
+// Eight floats (already divided by their scale) to eight E2M1 codes (round to
+// nearest even, saturating), the first in the lowest bits.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   uint32_t r;
   asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"

@@ -10,8 +10,9 @@
 // The weights are the MMA's M side and the tokens its N side: a unit of work
 // is 2 x 128 weight rows (product: 256 consecutive output features; swiglu:
 // 128 gate rows and the 128 up rows of the same features) times a run of up
-// to nmax rows of one expert, cut evenly and rounded up to 16, so that an
-// expert with few rows costs few MMA columns and no row is padded in memory.
+// to 96 rows of one expert, cut evenly and rounded up to 16, so that an expert
+// with few rows costs few MMA columns and no row is padded in memory.  Experts
+// of more than 96 rows on average run on CTA pairs (below).
 //
 //   warp 0      TMA: 256 elements of K a stage (128-byte swizzled rows) of both
 //               weight tiles and the token rows.
@@ -22,11 +23,23 @@
 //               asynchronous copies (the first row of a token run may be any)
 //               that land word (row 32 c + l) of 128 rows at 16 l + 4 c, the
 //               order in which tc_cp_scales reads them.  One warp for both
-//               chunks took 640-720 cycles a stage, more than the MMAs.
-//   warps 4-19  epilogue: four warps per lane quarter.  A lane is a feature and
-//               a warp's 32 lanes are one block of h: its magnitude is a warp
-//               reduction, the codes of 8 tokens and 8 features are exchanged
-//               by three shuffles.
+//               chunks took 640-720 cycles a stage, more than the MMAs; loads
+//               to registers two stages ahead and 16-byte shared stores in
+//               their place made the products of large experts 13-20% slower.
+//   warps 4-11  epilogue: two warps per lane quarter.  A lane is a feature and
+//               a warp's 32 lanes are one block of h: its largest magnitude
+//               and the exchange of 8 x 8 codes are shuffles.  16 warps were
+//               slower (product 284 -> 315 us at 384 experts of 165 rows).
+//
+// What bounds them, on a B200 under its 1 kW limit (random operands; a plain
+// copy of random data draws 0.88-0.97 kW there, 148 pJ a byte of HBM traffic):
+// experts of few rows stream their weights at the copy bandwidth (512 experts,
+// 640 rows, N = 4096, K = 1024: 115 us, 7.0 TB/s).  With many rows the power
+// limit binds: 64 experts x 512 rows, N = K = 4096 takes 350 us (3.1 PFLOP/s,
+// 1.37 GHz), of which the MMAs alone, on operands that are already there, take
+// 175 us at 0.99 kW and everything else without them 270 us at 0.99 kW.  Fewer
+// cycles (a look at the next stage's barrier during the MMAs) changed nothing.
+// DRAM reads are the operands once (164 MB of 160 at 16 experts x 512 rows).
 //
 // K need not be a multiple of 256: loads past its end read zeros, and the MMAs
 // past it are not issued.
@@ -56,7 +69,6 @@ constexpr int kStgRow = 80;                               // 64 bytes of feature
 constexpr uint32_t kStgBytes = 16 * kStgRow;              // per epilogue warp
 constexpr int kSmemAlign = 1024;
 constexpr int kSmemTail = 512;                            // barriers, TMEM slot, abort flag
-
 constexpr int64_t kMaxUnits = 1 << 30;
 
 enum OutKind { kOutBf16 = 0, kOutFp16 = 1, kOutFp32 = 2, kOutSwiglu = 3 };
@@ -192,29 +204,6 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, const
   const int64_t t0 = clock64();
   while (!mbar_try_wait(a, parity) && clock64() - t0 <= p.timeout_cycles) {
   }
-}
-
-// The epilogue's wait for an accumulator, of which it is a whole unit ahead:
-// one lane looks every 200 ns and the warp sleeps in between.
-__device__ __forceinline__ bool warp_nap(uint64_t* bar, uint32_t parity, int lane, volatile int* abort_flag,
-                                         const Params& p) {
-  int got = 1;
-  if (lane == 0) {
-    const uint32_t a = smem_u32(bar);
-    int64_t t0 = 0;
-    while (!mbar_try_wait(a, parity)) {
-      const int64_t now = clock64();
-      t0 = t0 == 0 ? now : t0;
-      if (*abort_flag || now - t0 > p.timeout_cycles) {
-        if (!*abort_flag) atomicOr(p.err, kDevErrTimeout);
-        *abort_flag = 1;
-        got = 0;
-        break;
-      }
-      __nanosleep(200);
-    }
-  }
-  return __shfl_sync(0xffffffffu, got, 0) != 0;
 }
 
 // One lane waits, the warp learns the outcome.
@@ -580,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int buf = static_cast<int>(count % kBufs);
       const uint32_t bpar = (count / kBufs) & 1u;
-      if (!warp_nap(&tfull[buf], bpar, lane, abort_flag, p)) break;
+      if (!warp_wait(&tfull[buf], bpar, lane, abort_flag, p)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                           static_cast<uint32_t>(buf * F::NA * F::NMAX);
@@ -799,6 +788,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < KB; ++kb) {
             ok = wait_phase(&full[stage], phase, abort_flag, p);
             if (!ok) break;
+            // The scales are in this CTA's shared memory and only its own
+            // tensor core reads them, once the leader has seen this arrival:
+            // ordered by the proxy fence, no cluster-scope release (which
+            // cost half of the rate).
             fence_proxy_async_smem();
             mbar_arrive_cluster(full_leader + 8u * stage);
             if (++stage == S) {
@@ -863,7 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int buf = static_cast<int>(count % kBufs);
       const uint32_t bpar = (count / kBufs) & 1u;
-      bool got_acc = warp_nap(&tfull[buf], bpar, lane, abort_flag, p);
+      bool got_acc = warp_wait(&tfull[buf], bpar, lane, abort_flag, p);
       if constexpr (SWIGLU) {
         // Both warps of an exchange go on, or neither does: they meet at its
         // barriers.  The slots of a unit are written again two units later.

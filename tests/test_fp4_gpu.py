@@ -427,3 +427,19 @@ def test_refusals_on_the_device():
     assert e.value.status == api.MOE_ERR_UNSUPPORTED
     torch.cuda.synchronize()
     assert bool((out == 3.0).all())
+
+
+def test_error_word_is_kept_by_products_and_cleared_by_the_sort():
+    """A timeout recorded in the workspace (by the bounded-wait self-test, 1 ms) survives products, not the next sort."""
+    rng = np.random.default_rng(10)
+    a, av = random_fp4(rng, 1, 8, 128)
+    w, wv = random_fp4(rng, 2, 64, 128)
+    ws = api.alloc_dispatch_workspace()
+    out = torch.empty(8, 64, device="cuda")
+    api.moe_debug_wait_timeout(ws, 1000000)
+    api.moe_matmul_fp4(a, dev(offsets_of([3, 5])), w, out, ws)
+    assert api.moe_device_status(ws) == api.MOE_ERR_DEVICE_TIMEOUT
+    assert np.allclose(out.cpu().numpy()[:3], av[0, :3] @ wv[0].T, rtol=1e-5)
+    idx = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    api.moe_sort_tokens(idx, torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty_like(idx), ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
