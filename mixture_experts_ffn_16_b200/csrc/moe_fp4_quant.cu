@@ -32,9 +32,11 @@ struct Eight;
 template <>
 struct Eight<float> {
   float4 a, b;
+  template <bool STREAM>
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4* v = reinterpret_cast<const float4*>(p);
+    a = STREAM ? __ldcs(v) : __ldg(v);
+    b = STREAM ? __ldcs(v + 1) : __ldg(v + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ uint32_t amax_bits() const {
@@ -52,8 +54,10 @@ struct Eight<float> {
 template <>
 struct Eight<__nv_bfloat16> {
   __nv_bfloat162 h[4];
+  template <bool STREAM>
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    *reinterpret_cast<uint4*>(h) = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4* v = reinterpret_cast<const uint4*>(p);
+    *reinterpret_cast<uint4*>(h) = STREAM ? __ldcs(v) : __ldg(v);
   }
   __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(h) = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ uint32_t amax_bits() const {
@@ -75,8 +79,10 @@ struct Eight<__nv_bfloat16> {
 template <>
 struct Eight<__half> {
   __half2 h[4];
+  template <bool STREAM>
   __device__ __forceinline__ void load(const __half* p) {
-    *reinterpret_cast<uint4*>(h) = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4* v = reinterpret_cast<const uint4*>(p);
+    *reinterpret_cast<uint4*>(h) = STREAM ? __ldcs(v) : __ldg(v);
   }
   __device__ __forceinline__ void zero() { *reinterpret_cast<uint4*>(h) = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ uint32_t amax_bits() const {
@@ -209,7 +215,9 @@ __device__ __forceinline__ int64_t scale_at(const Layout& l, int64_t row, int ch
 }
 
 // SLOTS: row = token; the codes and scales go to the rows that its k slots
-// have (slot_row), the token being read and quantised once.
+// have (slot_row), the token being read and quantised once.  Tokens and codes
+// then pass through the L2 as streams, so that the scale words, 4 bytes here
+// and there, can be gathered in it (360k rows of 7168: 470 -> 381 us).
 template <typename T, bool SLOTS, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __restrict__ scales,
@@ -223,7 +231,7 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
   for (int j = 0; j < kUnits; ++j) {
     int dr, u;
     if (locate<WHOLE>(l, s, 32 * j + lane, &dr, &u))
-      f[j].load(x0 + (dr * l.groups + u) * 8);
+      f[j].template load<SLOTS>(x0 + (dr * l.groups + u) * 8);
     else
       f[j].zero();
   }
@@ -264,7 +272,7 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
     for (int j = 0; j < k; ++j) {
       if (bin) {
         const uint32_t r = static_cast<uint32_t>(__ldg(bto + j));
-        if (r < R) c0[static_cast<size_t>(r) * (l.groups >> 2)] = block;
+        if (r < R) __stcs(c0 + static_cast<size_t>(r) * (l.groups >> 2), block);
       }
       if (sin) {
         const uint32_t r = static_cast<uint32_t>(__ldg(sto + j));
