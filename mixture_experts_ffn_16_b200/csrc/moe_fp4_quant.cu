@@ -32,11 +32,20 @@ struct Eight;
 template <>
 struct Eight<float> {
   float4 a, b;
+  // 32 bytes a lane in one access where the tensor allows it: two of 16 bytes
+  // each touch every sector (4097 x 7168 rows: 23.7 us to MXFP4 and 25.0 back,
+  // 21.8 and 22.9 this way).
   template <bool STREAM>
-  __device__ __forceinline__ void load(const float* p) {
+  __device__ __forceinline__ void load(const float* p, bool wide) {
     const float4* v = reinterpret_cast<const float4*>(p);
-    a = STREAM ? __ldcs(v) : __ldg(v);
-    b = STREAM ? __ldcs(v + 1) : __ldg(v + 1);
+    if (wide) {
+      asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w), "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                   : "l"(p));        // volatile: stays behind the wait for the kernel before
+    } else {
+      a = STREAM ? __ldcs(v) : __ldg(v);
+      b = STREAM ? __ldcs(v + 1) : __ldg(v + 1);
+    }
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ uint32_t amax_bits() const {
@@ -55,7 +64,7 @@ template <>
 struct Eight<__nv_bfloat16> {
   __nv_bfloat162 h[4];
   template <bool STREAM>
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) {
     const uint4* v = reinterpret_cast<const uint4*>(p);
     *reinterpret_cast<uint4*>(h) = STREAM ? __ldcs(v) : __ldg(v);
   }
@@ -80,7 +89,7 @@ template <>
 struct Eight<__half> {
   __half2 h[4];
   template <bool STREAM>
-  __device__ __forceinline__ void load(const __half* p) {
+  __device__ __forceinline__ void load(const __half* p, bool) {
     const uint4* v = reinterpret_cast<const uint4*>(p);
     *reinterpret_cast<uint4*>(h) = STREAM ? __ldcs(v) : __ldg(v);
   }
@@ -99,18 +108,24 @@ struct Eight<__half> {
     }
   }
 };
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(float* p, const float (&f)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+                 ::"f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "l"(p)
+                 : "memory");
+    return;
+  }
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8], bool) {
   uint4 v;
   __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
   *reinterpret_cast<uint4*>(p) = v;
 }
-__device__ __forceinline__ void store8(__half* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(__half* p, const float (&f)[8], bool) {
   uint4 v;
   __half2* h = reinterpret_cast<__half2*>(&v);
 #pragma unroll
@@ -175,6 +190,7 @@ struct Layout {
   uint64_t m64, g64;
   uint32_t m32;
   int P, groups, chunks, per_matrix;     // groups = K / 8; rows per matrix
+  bool wide;                             // x starts at a multiple of 32 bytes
 };
 
 // The groups of one warp: they start at group rem0 of row row0.  WHOLE: K is a
@@ -231,7 +247,7 @@ quantize_kernel(const T* __restrict__ x, uint4* __restrict__ codes, uint32_t* __
   for (int j = 0; j < kUnits; ++j) {
     int dr, u;
     if (locate<WHOLE>(l, s, 32 * j + lane, &dr, &u))
-      f[j].template load<SLOTS>(x0 + (dr * l.groups + u) * 8);
+      f[j].template load<SLOTS>(x0 + (dr * l.groups + u) * 8, l.wide);
     else
       f[j].zero();
   }
@@ -317,14 +333,15 @@ dequantize_kernel(const uint4* __restrict__ codes, const uint32_t* __restrict__ 
         f[2 * i] = q.x * sc;
         f[2 * i + 1] = q.y * sc;
       }
-      store8(x0 + (dr * l.groups + u) * 8, f);
+      store8(x0 + (dr * l.groups + u) * 8, f, l.wide);
     }
   }
 }
 
-Layout make_layout(int64_t rows, int per_matrix, int K) {
+Layout make_layout(int64_t rows, int per_matrix, int K, const void* x) {
   Layout l;
   l.rows = rows;
+  l.wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0;
   l.per_matrix = per_matrix;
   l.chunks = (K + 127) / 128;
   l.groups = K / 8;
@@ -342,7 +359,7 @@ dim3 layout_grid(const Layout& l) {
 template <typename T, bool SLOTS>
 int quantize_t(int64_t rows, int per_matrix, int K, const void* x, const int32_t* slot_row, int k, void* codes,
                void* scales, cudaStream_t st) {
-  const Layout l = make_layout(rows, per_matrix, K);
+  const Layout l = make_layout(rows, per_matrix, K, x);
   const auto kern = K % 1024 ? quantize_kernel<T, SLOTS, false> : quantize_kernel<T, SLOTS, true>;
   return launch_chained(kern, layout_grid(l), dim3(kThreads), 0, st, static_cast<const T*>(x),
                         static_cast<uint4*>(codes), static_cast<uint32_t*>(scales), l, slot_row, k) == cudaSuccess
@@ -353,7 +370,7 @@ int quantize_t(int64_t rows, int per_matrix, int K, const void* x, const int32_t
 template <typename T>
 int dequantize_t(int64_t rows, int per_matrix, int K, const void* codes, const void* scales, void* x,
                  cudaStream_t st) {
-  const Layout l = make_layout(rows, per_matrix, K);
+  const Layout l = make_layout(rows, per_matrix, K, x);
   const auto kern = K % 1024 ? dequantize_kernel<T, false> : dequantize_kernel<T, true>;
   return launch_chained(kern, layout_grid(l), dim3(kThreads), 0, st,
                         static_cast<const uint4*>(codes), static_cast<const uint32_t*>(scales), static_cast<T*>(x),

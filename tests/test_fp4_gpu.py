@@ -95,6 +95,30 @@ def test_quantize_extremes(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [192, 2048])
+def test_tensors_that_start_at_16_bytes(K, dtype):
+    """x, codes and scales at addresses that are multiples of 16 bytes only give what aligned ones give."""
+    def off16(t):
+        room = torch.empty(t.numel() * t.element_size() + 16, dtype=torch.uint8, device="cuda")
+        view = room[16:].view(t.dtype).view(t.shape)
+        assert view.data_ptr() % 32 == 16
+        return view.copy_(t)
+
+    rng = np.random.default_rng(K)
+    x = hard_rows(rng, 9, K, dtype)[None].cuda()
+    q, back = api.fp4_empty(1, 9, K), torch.empty_like(x)
+    api.moe_quantize_fp4(x, *q)
+    api.moe_dequantize_fp4(*q, back)
+    x2, q2, back2 = off16(x), tuple(map(off16, api.fp4_empty(1, 9, K))), off16(back.clone().zero_())
+    api.moe_quantize_fp4(x2, *q2)
+    api.moe_dequantize_fp4(*q2, back2)
+    assert torch.equal(q[0], q2[0]) and torch.equal(q[1], q2[1]) and torch.equal(back, back2)
+    rows = torch.arange(9, dtype=torch.int32, device="cuda").view(9, 1)
+    api.moe_dispatch_fp4(x2[0], off16(rows), tuple(t.fill_(1) for t in q2))
+    assert torch.equal(q[0], q2[0]) and torch.equal(q[1], q2[1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,d,k,E", [(1, 64, 1, 1), (5, 192, 3, 4), (37, 4096, 8, 20), (3, 8256, 32, 40),
                                      (6, 1024, 32, 7)])
 def test_dispatch_fp4_is_quantize_then_dispatch(T, d, k, E, dtype):
