@@ -449,7 +449,9 @@ def moe_debug_wait_timeout(workspace, timeout_ns, stream=None):
 
 # ---- Token dispatch and MXFP4 experts ----
 # Sizes come from the tensors.  An MXFP4 tensor is a (codes uint8 [G, rows, K/2],
-# scales uint8 [G, ceil(K/128), rows, 4]) pair; fp4_empty allocates one.
+# scales uint8 [G, ceil(K/128), rows, 4]) pair; fp4_empty allocates one.  Scales
+# kept row by row, [G, rows, K/32] with K a multiple of 128, become that by
+# s.view(G, rows, K // 128, 4).transpose(1, 2).contiguous().
 
 def alloc_dispatch_workspace(device=None):
     """The workspace of moe_sort_tokens and the MXFP4 products, its error word cleared."""

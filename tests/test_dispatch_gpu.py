@@ -242,3 +242,34 @@ def test_gradients_against_differences(dtype):
             size = np.abs(has[t] * wv[t] * gv[t, i]).sum()
             # each of k terms rounded to the type, k additions, one more rounding
             assert abs(dx[t, i].item() - want) <= (2 * half + (k + 1) * 2.0 ** -24) * 1.01 * size + 1e-12
+
+
+def test_the_largest_sort_and_dispatch():
+    """T = 4,194,304 tokens, k = 32: 134,217,728 rows, against a stable sort; the last tokens are dropped."""
+    T, k, E, d = 1 << 22, 32, 2048, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32, device="cuda")
+    idx[-5:] = -1
+    offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    slot_row = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    ws = api.alloc_dispatch_workspace()
+    api.moe_sort_tokens(idx, offsets, slot_row, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    key = idx.view(-1).clone()
+    key[key < 0] = E
+    order = torch.sort(key, stable=True).indices
+    n = (T - 5) * k
+    assert torch.equal(slot_row.view(-1)[order[:n]].long(), torch.arange(n, device="cuda"))
+    assert bool((slot_row[-5:] == -1).all())
+    counts = torch.bincount(key[:n], minlength=E)
+    assert torch.equal(offsets[1:].long(), counts.cumsum(0)) and offsets[0].item() == 0
+    del order, key
+    x = torch.randn(T, d, device="cuda").bfloat16()
+    xs = torch.zeros(T * k, d, dtype=torch.bfloat16, device="cuda")
+    api.moe_dispatch(x, slot_row, xs)
+    for j in (0, 13, 31):
+        assert torch.equal(xs[slot_row[:-5, j].long()], x[:-5])
+    assert not bool(xs[n:].any())
+    dx = torch.empty_like(x)
+    api.moe_dispatch_backward(xs, slot_row, dx)         # 32 equal rows: 32 x, exact
+    assert torch.equal(dx[:-5], 32 * x[:-5]) and not bool(dx[-5:].any())

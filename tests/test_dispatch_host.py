@@ -107,3 +107,15 @@ def test_fp4_empty_shapes():
     assert codes.shape == (3, 5, 96) and scales.shape == (3, 2, 5, 4)
     ws = api.alloc_dispatch_workspace("cpu")
     assert ws.numel() == api.DISPATCH_WORKSPACE_BYTES and not ws.any()
+
+
+def test_row_by_row_scales_become_the_layout():
+    """The rearrangement that the binding's notes give, against the oracle's."""
+    import numpy as np
+
+    import fp4_ref as ref
+    rng = np.random.default_rng(0)
+    byte = rng.integers(0, 255, (2, 5, 8), dtype=np.uint8)               # K = 256
+    want = ref.pack(np.zeros((2, 5, 256), dtype=int), byte)[1]
+    got = torch.from_numpy(byte).view(2, 5, 2, 4).transpose(1, 2).contiguous()
+    assert np.array_equal(got.numpy(), want)

@@ -467,3 +467,67 @@ def test_error_word_is_kept_by_products_and_cleared_by_the_sort():
     idx = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
     api.moe_sort_tokens(idx, torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty_like(idx), ws)
     assert api.moe_device_status(ws) == api.MOE_OK
+
+
+@pytest.mark.parametrize("most", [3, 260])               # single CTAs, CTA pairs
+def test_as_many_experts_as_there_may_be(most):
+    """E = 2048: the products' tables at their largest, many experts empty."""
+    rng = np.random.default_rng(most)
+    counts = rng.integers(0, most, 2048)
+    counts[rng.random(2048) < 0.2] = 0
+    off = offsets_of(counts)
+    rows, N, K = int(off[-1]), 64, 64
+    a, av = random_fp4(rng, 1, rows, K)
+    w, wv = random_fp4(rng, 2048, N, K)
+    out, ws = torch.empty(rows, N, device="cuda"), api.alloc_dispatch_workspace()
+    api.moe_matmul_fp4(a, dev(off), w, out, ws)
+    h = api.fp4_empty(1, rows, N)
+    api.moe_swiglu_fp4(a, dev(off), w, w, h, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    got = out.double().cpu().numpy()
+    codes, scales = ref.unpack(h[0].cpu().numpy())[0], ref.rows_of_scales(h[1].cpu().numpy(), N)[0]
+    g, size = np.empty((rows, N)), np.empty((rows, N))
+    for e in range(2048):
+        r = slice(off[e], off[e + 1])
+        g[r], size[r] = av[0, r] @ wv[e].T, np.abs(av[0, r]) @ np.abs(wv[e]).T
+    add = 2.0 ** -22 * size
+    assert ref.within(got, g, add + ref.half_step(out.dtype, np.abs(g) + add))
+    check_swiglu(codes, scales, g, g, size, size, K)
+
+
+def test_the_widest_rows():
+    """K = 65,536, the longest accumulation: 256 stages for a unit."""
+    rng = np.random.default_rng(2)
+    for counts in ([2, 1], [120, 100]):
+        off, N, K = offsets_of(counts), 64, 65536
+        rows = int(off[-1])
+        a, av = random_fp4(rng, 1, rows, K)
+        w, wv = random_fp4(rng, 2, N, K)
+        out, ws = torch.empty(rows, N, device="cuda"), api.alloc_dispatch_workspace()
+        api.moe_matmul_fp4(a, dev(off), w, out, ws)
+        assert api.moe_device_status(ws) == api.MOE_OK
+        for e in range(2):
+            r = slice(off[e], off[e + 1])
+            want, size = av[0, r] @ wv[e].T, np.abs(av[0, r]) @ np.abs(wv[e]).T
+            add = (K / 64) * 2.0 ** -22 * size
+            assert ref.within(out[r].double().cpu().numpy(), want, add + ref.half_step(out.dtype, np.abs(want) + add))
+
+
+def test_the_most_rows():
+    """134,217,728 rows (the most a call takes) on 3 experts, sampled."""
+    rows, N, K = 1 << 27, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = (torch.randint(0, 256, (1, rows, K // 2), generator=g, dtype=torch.uint8, device="cuda"),
+         torch.full((1, 1, rows, 4), 127, dtype=torch.uint8, device="cuda"))
+    rng = np.random.default_rng(1)
+    w, wv = random_fp4(rng, 3, N, K)
+    off = np.array([0, 5, 70_000_003, rows - 2], dtype=np.int32)
+    out = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    ws = api.alloc_dispatch_workspace()
+    api.moe_matmul_fp4(a, dev(off), w, out, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    for r in (0, 4, 5, 70_000_002, 70_000_003, 100_000_000, rows - 3):
+        x = ref.VALUES[ref.unpack(a[0][0, r].cpu().numpy())]
+        want = wv[np.searchsorted(off, r, side="right") - 1] @ x
+        assert ref.within(out[r].double().cpu().numpy(), want, ref.half_step(out.dtype, want) + 2.0 ** -22 * 64 * 36)
+    assert not bool(out[rows - 2:].any())
