@@ -509,13 +509,21 @@ def _on(stream, dev):
 def _fp4_dims(q, name):
     if not isinstance(q, (tuple, list)) or len(q) != 2:
         raise TypeError(f"{name}: expected a (codes, scales) pair")
-    G, rows, half = _dims(q[0], 3, name + ".codes")
+    G, rows, half = _dims(q[0], 3, name)
     return G, rows, 2 * half
 
 
 def _f4(q, G, rows, K, name, dev):
-    return ctypes.byref(MoeFp4Tensor(_t(q[0], torch.uint8, (G, rows, K // 2), name + ".codes", dev),
-                                     _t(q[1], torch.uint8, (G, (K + 127) // 128, rows, 4), name + ".scales", dev)))
+    """moe_fp4_tensor of a (codes, scales) pair of G x rows x K values on device `dev` (the call passes its address)."""
+    _fp4_dims(q, name)
+    c, s = q
+    u8 = torch.uint8
+    if (type(s) is torch.Tensor and c.dtype is u8 and s.dtype is u8 and c.shape == (G, rows, K // 2)
+            and s.shape == (G, (K + 127) // 128, rows, 4) and c.is_contiguous() and s.is_contiguous()
+            and c.get_device() == s.get_device() == dev >= 0):
+        return MoeFp4Tensor(c.data_ptr(), s.data_ptr())
+    return MoeFp4Tensor(_t(c, u8, (G, rows, K // 2), name + ".codes", dev),
+                        _t(s, u8, (G, (K + 127) // 128, rows, 4), name + ".scales", dev))
 
 
 def moe_sort_tokens(topk_idx, offsets, slot_row, workspace, stream=None):
@@ -589,10 +597,10 @@ def moe_dispatch_fp4(x, slot_row, x_sorted, stream=None):
     """moe_dispatch of x's MXFP4 form: x_sorted is an MXFP4 tensor (G = 1) of T * k rows."""
     (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
     dev, dt = _dev(x), _dtype(x, "x")
-    _fp4_dims(x_sorted, "x_sorted")
+    q = _f4(x_sorted, 1, T * k, d, "x_sorted", dev)
     _check(load().moe_dispatch_fp4(T, k, d, dt, _t(x, x.dtype, None, "x", dev),
-                                   _t(slot_row, torch.int32, (T, k), "slot_row", dev),
-                                   _f4(x_sorted, 1, T * k, d, "x_sorted", dev), _on(stream, dev)), "moe_dispatch_fp4")
+                                   _t(slot_row, torch.int32, (T, k), "slot_row", dev), q, _on(stream, dev)),
+           "moe_dispatch_fp4")
 
 
 def moe_matmul_fp4(a, offsets, W, out, workspace, stream=None):
@@ -610,8 +618,6 @@ def moe_matmul_fp4(a, offsets, W, out, workspace, stream=None):
 def moe_swiglu_fp4(a, offsets, W_gate, W_up, h, workspace, stream=None):
     """h[r] = SiLU(a[r] W_gate[e]^T) * (a[r] W_up[e]^T), as MXFP4 (G = 1)."""
     (_, rows, K), (E, f, _) = _fp4_dims(a, "a"), _fp4_dims(W_gate, "W_gate")
-    _fp4_dims(W_up, "W_up")
-    _fp4_dims(h, "h")
     dev = _dev(a[0])
     _check(load().moe_swiglu_fp4(rows, E, f, K, _f4(a, 1, rows, K, "a", dev),
                                  _t(offsets, torch.int32, (E + 1,), "offsets", dev),
