@@ -65,7 +65,11 @@ class MoeFp4Tensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+_FAST_CALLS = ["sort_tokens", "dispatch", "dispatch_backward", "undispatch", "undispatch_backward", "quantize_fp4",
+               "dequantize_fp4", "dispatch_fp4", "matmul_fp4", "swiglu_fp4"]   # csrc/fastcall.cpp's order
+
 _lib = None
+_fastcall = None
 
 
 def load():
@@ -139,6 +143,25 @@ def load():
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def _fast():
+    """The native part of the binding (csrc/fastcall.cpp), given the library's addresses once."""
+    global _fastcall
+    if _fastcall is None:
+        lib = load()
+        from . import _fastcall as native
+        native.bind(tuple(ctypes.cast(getattr(lib, "moe_" + n), ctypes.c_void_p).value for n in _FAST_CALLS))
+        _fastcall = native
+    return _fastcall
+
+
+def _done(status, where):
+    """Whether the native part made the call (None: it did not)."""
+    if status is None:
+        return False
+    _check(status, where)
+    return True
 
 
 def status_string(status):
@@ -448,6 +471,8 @@ def moe_debug_wait_timeout(workspace, timeout_ns, stream=None):
 
 
 # ---- Token dispatch and MXFP4 experts ----
+# A call is made by the native part of the binding where every argument is what
+# it should be and no stream is given; else here, which says what is wrong.
 # Sizes come from the tensors.  An MXFP4 tensor is a (codes uint8 [G, rows, K/2],
 # scales uint8 [G, ceil(K/128), rows, 4]) pair; fp4_empty allocates one.  Scales
 # kept row by row, [G, rows, K/32] with K a multiple of 128, become that by
@@ -528,6 +553,8 @@ def _f4(q, G, rows, K, name, dev):
 
 def moe_sort_tokens(topk_idx, offsets, slot_row, workspace, stream=None):
     """Rows of the (token, slot) pairs in expert order: offsets [E+1], slot_row [T, k] (-1: no expert)."""
+    if stream is None and _done(_fast().sort_tokens(topk_idx, offsets, slot_row, workspace), "moe_sort_tokens"):
+        return
     T, k = _dims(topk_idx, 2, "topk_idx")
     E = _dims(offsets, 1, "offsets")[0] - 1
     dev, i32 = _dev(topk_idx), torch.int32
@@ -539,6 +566,8 @@ def moe_sort_tokens(topk_idx, offsets, slot_row, workspace, stream=None):
 
 def moe_dispatch(x, slot_row, x_sorted, stream=None):
     """x_sorted[slot_row[t, j]] = x[t]."""
+    if stream is None and _done(_fast().dispatch(x, slot_row, x_sorted), "moe_dispatch"):
+        return
     (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
     dev, dt = _dev(x), _dtype(x, "x")
     _check(load().moe_dispatch(T, k, d, dt, _t(x, x.dtype, None, "x", dev),
@@ -548,6 +577,8 @@ def moe_dispatch(x, slot_row, x_sorted, stream=None):
 
 def moe_dispatch_backward(dx_sorted, slot_row, dx, stream=None):
     """dx[t] = sum_j dx_sorted[slot_row[t, j]]."""
+    if stream is None and _done(_fast().dispatch_backward(dx_sorted, slot_row, dx), "moe_dispatch_backward"):
+        return
     (T, d), k = _dims(dx, 2, "dx"), _dims(slot_row, 2, "slot_row")[1]
     dev, dt = _dev(dx), _dtype(dx, "dx")
     _check(load().moe_dispatch_backward(T, k, d, dt, _t(dx_sorted, dx.dtype, (T * k, d), "dx_sorted", dev),
@@ -557,6 +588,8 @@ def moe_dispatch_backward(dx_sorted, slot_row, dx, stream=None):
 
 def moe_undispatch(y, slot_row, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] y[slot_row[t, j]]."""
+    if stream is None and _done(_fast().undispatch(y, slot_row, topk_w, out), "moe_undispatch"):
+        return
     (T, d), k = _dims(out, 2, "out"), _dims(slot_row, 2, "slot_row")[1]
     dev, dt = _dev(out), _dtype(out, "out")
     _check(load().moe_undispatch(T, k, d, dt, _t(y, out.dtype, (T * k, d), "y", dev),
@@ -567,6 +600,8 @@ def moe_undispatch(y, slot_row, topk_w, out, stream=None):
 
 def moe_undispatch_backward(dout, y, slot_row, topk_w, dy, dw, stream=None):
     """dy[slot_row[t, j]] = topk_w[t, j] dout[t]; dw[t, j] = <dout[t], y[slot_row[t, j]]>."""
+    if stream is None and _done(_fast().undispatch_backward(dout, y, slot_row, topk_w, dy, dw), "moe_undispatch_backward"):
+        return
     (T, d), k = _dims(dout, 2, "dout"), _dims(slot_row, 2, "slot_row")[1]
     dev, dt, f32 = _dev(dout), _dtype(dout, "dout"), torch.float32
     _check(load().moe_undispatch_backward(T, k, d, dt, _t(dout, dout.dtype, None, "dout", dev),
@@ -579,6 +614,8 @@ def moe_undispatch_backward(dout, y, slot_row, topk_w, dy, dw, stream=None):
 
 def moe_quantize_fp4(x, codes, scales, stream=None):
     """x [G, rows, K] (bf16, fp16 or fp32) to MXFP4."""
+    if stream is None and _done(_fast().quantize_fp4(x, codes, scales), "moe_quantize_fp4"):
+        return
     G, rows, K = _dims(x, 3, "x")
     dev, dt = _dev(x), _dtype(x, "x")
     _check(load().moe_quantize_fp4(G, rows, K, dt, _t(x, x.dtype, None, "x", dev),
@@ -587,6 +624,8 @@ def moe_quantize_fp4(x, codes, scales, stream=None):
 
 def moe_dequantize_fp4(codes, scales, x, stream=None):
     """MXFP4 back to x [G, rows, K] (bf16, fp16 or fp32)."""
+    if stream is None and _done(_fast().dequantize_fp4(codes, scales, x), "moe_dequantize_fp4"):
+        return
     G, rows, K = _dims(x, 3, "x")
     dev, dt = _dev(x), _dtype(x, "x")
     _check(load().moe_dequantize_fp4(G, rows, K, dt, _f4((codes, scales), G, rows, K, "q", dev),
@@ -595,6 +634,8 @@ def moe_dequantize_fp4(codes, scales, x, stream=None):
 
 def moe_dispatch_fp4(x, slot_row, x_sorted, stream=None):
     """moe_dispatch of x's MXFP4 form: x_sorted is an MXFP4 tensor (G = 1) of T * k rows."""
+    if stream is None and _done(_fast().dispatch_fp4(x, slot_row, x_sorted), "moe_dispatch_fp4"):
+        return
     (T, d), k = _dims(x, 2, "x"), _dims(slot_row, 2, "slot_row")[1]
     dev, dt = _dev(x), _dtype(x, "x")
     q = _f4(x_sorted, 1, T * k, d, "x_sorted", dev)
@@ -605,6 +646,8 @@ def moe_dispatch_fp4(x, slot_row, x_sorted, stream=None):
 
 def moe_matmul_fp4(a, offsets, W, out, workspace, stream=None):
     """out[r] = a[r] W[e]^T for the rows offsets[e] <= r < offsets[e+1] of every expert e."""
+    if stream is None and _done(_fast().matmul_fp4(a, offsets, W, out, workspace), "moe_matmul_fp4"):
+        return
     (_, rows, K), (E, N, _) = _fp4_dims(a, "a"), _fp4_dims(W, "W")
     _dims(out, 2, "out")
     dev, dt = _dev(out), _dtype(out, "out")
@@ -617,6 +660,8 @@ def moe_matmul_fp4(a, offsets, W, out, workspace, stream=None):
 
 def moe_swiglu_fp4(a, offsets, W_gate, W_up, h, workspace, stream=None):
     """h[r] = SiLU(a[r] W_gate[e]^T) * (a[r] W_up[e]^T), as MXFP4 (G = 1)."""
+    if stream is None and _done(_fast().swiglu_fp4(a, offsets, W_gate, W_up, h, workspace), "moe_swiglu_fp4"):
+        return
     (_, rows, K), (E, f, _) = _fp4_dims(a, "a"), _fp4_dims(W_gate, "W_gate")
     dev = _dev(a[0])
     _check(load().moe_swiglu_fp4(rows, E, f, K, _f4(a, 1, rows, K, "a", dev),

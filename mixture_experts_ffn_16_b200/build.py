@@ -1,16 +1,20 @@
 """Build libmoe.so in-tree: every .cu under csrc/ compiled for sm_100a with nvcc
 and linked into one shared library (CUDA runtime linked statically, so the
 library loads on a machine without a GPU driver; it needs the driver only
-when a kernel is launched)."""
+when a kernel is launched).  And _fastcall.so, the Python binding's native
+part (csrc/fastcall.cpp), compiled with the host compiler against torch's
+headers; torch's libraries are in the process when it is imported."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
+FAST = os.path.join(HERE, "_fastcall.so")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
@@ -29,14 +33,39 @@ def _deps():
                               if f.endswith((".cuh", ".h"))) + [os.path.join(INCLUDE, "moe.h")]
 
 
-def up_to_date():
-    if not os.path.exists(LIB):
+def _newer(out, deps):
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def up_to_date():
+    return _newer(LIB, _deps())
+
+
+def build_fastcall(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "fastcall.cpp")
+    if not force and _newer(FAST, [src, os.path.join(INCLUDE, "moe.h")]):
+        return FAST
+    import torch
+    inc, libs = (os.path.join(os.path.dirname(torch.__file__), d) for d in ("include", "lib"))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, FAST)
+    return FAST
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_fastcall(force, verbose)
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
