@@ -46,19 +46,20 @@ __device__ __forceinline__ int ld_cluster(uint32_t cluster_addr) {
   return v;
 }
 
-// One cluster sorts all slots.  Warp w of CTA c owns the c * WARPS + w-th
-// run of consecutive slots.  Pass 1 counts each warp's slots per expert in
+// One cluster sorts all slots.  Warp w < active of CTA c owns the c * active +
+// w-th run of consecutive slots.  Pass 1 counts each warp's slots per expert in
 // shared memory; prefix sums over warps, then (through distributed shared
 // memory) over CTAs, then over experts give each (warp, expert) its first
 // row; pass 2 walks the slots again and places them, 32 at a time, each
 // behind the lower lanes with the same expert (each lane sets its bit in the
 // expert's mask): the order of slots inside an expert is kept.  One launch
 // instead of the count / scan / scatter of three.  Bound by the instructions
-// of pass 2 on the cluster's SMs; 65k slots of 256 experts took 15.1 us with a
-// warp match for the lanes of one expert, 11.0 us with a vote per bit.
+// of pass 2 on the cluster's SMs: 65k slots of 256 experts 7.7 us (15.1 us with
+// a warp match for the lanes of one expert, 11.0 us with a vote per bit), 360k
+// of 896 experts 29 us; 640 slots of 512 experts 3.1 us.
 template <int WARPS>
 __global__ void __launch_bounds__(32 * WARPS)
-sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t* __restrict__ offsets,
+sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int active, int32_t* __restrict__ offsets,
             int32_t* __restrict__ slot_row, uint32_t* __restrict__ err) {
   constexpr int kThreads = 32 * WARPS, kPer = sort_experts(WARPS) / kThreads;   // kPer: experts per thread
   extern __shared__ int32_t sm[];
@@ -68,7 +69,7 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   __shared__ int32_t wsum[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank(), ctas = cluster_nctas();
-  for (int i = tid; i < WARPS * E; i += kThreads) {
+  for (int i = tid; i < active * E; i += kThreads) {
     hist[i] = 0;
     masks[i] = 0;
   }
@@ -77,7 +78,7 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   __syncthreads();
 
   int32_t* mine = hist + warp * E;
-  const int64_t lo = static_cast<int64_t>(rank * WARPS + warp) * run;
+  const int64_t lo = warp < active ? static_cast<int64_t>(rank * active + warp) * run : n;
   const int begin = static_cast<int>(min(lo, static_cast<int64_t>(n)));
   const int end = static_cast<int>(min(lo + run, static_cast<int64_t>(n)));
   // The loads of a batch are issued before any is used.
@@ -98,15 +99,19 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
   __syncthreads();
   for (int e = tid; e < E; e += kThreads) {
     int s = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
+#pragma unroll 4
+    for (int w = 0; w < active; ++w) {
       const int c = hist[w * E + e];
       hist[w * E + e] = s;
       s += c;
     }
     total[e] = s;
   }
-  cluster_sync();
+  const bool alone = ctas == 1;
+  if (alone)
+    __syncthreads();
+  else
+    cluster_sync();
 
   // thread t: experts t * per .. + per - 1
   const int per = (E + kThreads - 1) / kThreads;
@@ -117,11 +122,15 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
     below[q] = all[q] = 0;
     const int e = tid * per + q;
     if (q < per && e < E) {
+      if (alone) {
+        all[q] = total[e];
+      } else {
 #pragma unroll
-      for (uint32_t c = 0; c < kSortMaxCluster; ++c) {
-        const int v = c < ctas ? ld_cluster(mapa_shared(smem_u32(total + e), c)) : 0;
-        if (c < rank) below[q] += v;
-        all[q] += v;
+        for (uint32_t c = 0; c < kSortMaxCluster; ++c) {
+          const int v = c < ctas ? ld_cluster(mapa_shared(smem_u32(total + e), c)) : 0;
+          if (c < rank) below[q] += v;
+          all[q] += v;
+        }
       }
       sum += all[q];
     }
@@ -133,7 +142,10 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
     if (lane >= o) inc += v;
   }
   if (lane == 31) wsum[warp] = inc;
-  cluster_sync();      // every CTA's reads of `total` are done; wsum is written
+  if (alone)
+    __syncthreads();
+  else
+    cluster_sync();    // every CTA's reads of `total` are done; wsum is written
   int base = inc - sum;
   for (int w = 0; w < warp; ++w) base += wsum[w];
 #pragma unroll
@@ -141,7 +153,8 @@ sort_kernel(const int32_t* __restrict__ topk_idx, int n, int E, int run, int32_t
     const int e = tid * per + q;
     if (q < per && e < E) {
       if (rank == 0) offsets[e] = base;
-      for (int w = 0; w < WARPS; ++w) hist[w * E + e] += base + below[q];     // first row of each warp's
+#pragma unroll 4
+      for (int w = 0; w < active; ++w) hist[w * E + e] += base + below[q];    // first row of each warp's
       base += all[q];
       if (rank == 0 && e == E - 1) offsets[E] = base;
     }
@@ -419,7 +432,12 @@ static int launch_sort(int n, int E, const int32_t* topk_idx, int32_t* offsets, 
   // cluster size.
   int ctas = 1;
   while (ctas < kSortMaxCluster && static_cast<int64_t>(ctas) * 32 * WARPS * kSortBatch < n) ctas *= 2;
-  const int warps = ctas * WARPS;
+  // Of one CTA, as many warps as have half a batch each: the counters of every
+  // warp are cleared and summed, which is most of the work of a small sort.
+  int active = WARPS;
+  if (ctas == 1) active = (n + 32 * kSortBatch / 2 - 1) / (32 * kSortBatch / 2);
+  active = active < WARPS ? active : WARPS;
+  const int warps = ctas * active;
   const int run = static_cast<int>((static_cast<int64_t>(n) + warps * 32 - 1) / (warps * 32)) * 32;
   static std::atomic<int> limit[64];
   const int rc = raise_smem_limit(sort_kernel<WARPS>, limit,
@@ -439,7 +457,7 @@ static int launch_sort(int n, int E, const int32_t* topk_idx, int32_t* offsets, 
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return ok_or_cuda(cudaLaunchKernelEx(&cfg, sort_kernel<WARPS>, topk_idx, n, E, run, offsets, slot_row, err));
+  return ok_or_cuda(cudaLaunchKernelEx(&cfg, sort_kernel<WARPS>, topk_idx, n, E, run, active, offsets, slot_row, err));
 }
 
 int launch_sort_tokens(int T, int k, int E, const int32_t* topk_idx, int32_t* offsets, int32_t* slot_row,
