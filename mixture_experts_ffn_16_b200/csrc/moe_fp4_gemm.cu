@@ -103,11 +103,21 @@ struct Form {
   static constexpr uint32_t kStage = kScaleOff + kChunks * kChunkScales;
   static constexpr uint32_t kStg = STG_;                             // epilogue staging
   static constexpr uint32_t kSfBase = kTmemCols - S * 4 * kChunks;   // its columns behind the accumulators
+  static constexpr int kPool = kSfBase & ~31u;                       // columns for accumulators
   static constexpr uint32_t kFixed = kSmemAlign + S * kStage + kStg + kSmemTail;
   static_assert(kStage % 1024 == 0 && kTokOff % 1024 == 0, "swizzled tiles start at multiples of 1024");
-  static_assert(kBufs * NA * NMAX <= static_cast<int>(kSfBase), "tensor memory");
+  static_assert(NA * NMAX <= kPool, "tensor memory");
   static_assert(kFixed + 2 * 4 * (kMaxE + 1) <= 232448, "shared memory, with the tables of kMaxE experts");
 };
+
+// Columns of an accumulator of n tokens, and where the one in place 0 or 1
+// starts: at either end of the pool.  Two neighbouring units that do not fit
+// beside each other take turns.
+__device__ __forceinline__ int acc_cols(int n) { return (n + 31) & ~31; }
+template <class F>
+__device__ __forceinline__ uint32_t acc_at(int buf, int n) {
+  return buf ? static_cast<uint32_t>(F::kPool - acc_cols(n)) : 0u;
+}
 
 template <class F>
 __device__ __forceinline__ int runs_of(int rows) {
@@ -374,6 +384,7 @@ __device__ __forceinline__ void issue_stage(uint32_t a_lo, uint32_t b_lo, uint64
 // columns: within 3%), and at 64 rows 64-token runs cost 15% (two runs for
 // every second expert).
 using Single = Form<2, 96, 96, 4, kEpiWarps * kStgBytes>;
+static_assert(kBufs * Single::NA * Single::NMAX <= Single::kPool, "both accumulators");
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_constant__ Params p) {
@@ -615,10 +626,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 }
 
 // The form for large experts, on CTA pairs (cta_group::2): 256 weight rows, 128
-// per CTA, times runs of up to 192 tokens, of which each CTA loads half; two
-// accumulators of 192 columns, so the epilogue overlaps the next unit.  Per
-// multiply-add it moves 2/3 of the bytes of the single CTA's 256 x 96 units
-// into shared memory, and half the MMAs are issued.
+// per CTA, times runs of up to 256 tokens, of which each CTA loads half.  Per
+// multiply-add that moves half of the bytes of the single CTA's 256 x 96 units
+// into shared memory, with a quarter of the MMAs.  The scales leave 384
+// columns of tensor memory for two accumulators: of 192 each they lie side by
+// side and the epilogue overlaps the next unit; a longer one and its neighbour
+// share columns, which the epilogue reads first and reports before the rest.
+// Against runs of up to 192 in two fixed places, 32 experts of 160 / 256 / 320
+// / 512 / 2048 rows, N = 2048, K = 4096: 36.7 / 55.9 / 61.7 / 93.0 / 311 us
+// there, 36.4 / 46.9 / 62.2 / 84.0 / 285 us this way (without the early report
+// longer runs gained nothing at 512 rows).
 //   product: CTA r has output features 128 r .. of the unit's 256.
 //   swiglu:  CTA r has features 64 r .. of the unit's 128, their gate rows in
 //            lanes 0..63 and their up rows in lanes 64..127.  A gate warp and
@@ -632,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 // cluster-scope release waits for the copies of later stages too.)
 constexpr uint32_t kXchBytes = 2 * 2 * 32 * 16 * 4;       // per warp pair: 2 buffers x 2 directions x 32 lanes x 16 floats
 
-using Pair = Form<1, 192, 96, 5, kEpiWarps / 2 * kXchBytes>;
+using Pair = Form<1, 256, 128, 5, kEpiWarps / 2 * kXchBytes>;
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -641,6 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr bool SWIGLU = KIND == kOutSwiglu;
   constexpr int kCtaFeats = SWIGLU ? kTileRows / 2 : kTileRows;      // output features per CTA
   constexpr int kRowsPerWb = 2 * kCtaFeats;
+  constexpr int kTwoFit = F::kPool / 2;      // columns of which two accumulators fit side by side
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + (kSmemAlign - 1)) & ~static_cast<uintptr_t>(kSmemAlign - 1));
@@ -650,7 +668,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + kBufs;
-  uint64_t* drain = tempty + kBufs;
+  uint64_t* tpart = tempty + kBufs;
+  uint64_t* drain = tpart + kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int64_t* wsum = reinterpret_cast<int64_t*>(tmem_slot + 2);
@@ -670,6 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(tfull + b, 1);
       mbar_init(tempty + b, 2 * kEpiWarps);
+      mbar_init(tpart + b, 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -692,6 +712,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int KB = (p.K + kStageK - 1) / kStageK;
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);       // + 8 * stage
   const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);   // + 8 * buffer
+  const uint32_t tpart_leader = mapa_shared(smem_u32(tpart), 0);
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
@@ -737,8 +758,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (leader)
     if (rank == 0) {
-      int stage = 0;
-      uint32_t phase = 0, count = 0;
+      int stage = 0, before = 0;         // columns of the unit before
+      uint32_t phase = 0, count = 0, part_phase = 3;     // bit: parity of the last early report of a place
       bool any = false, ok = true;
       const uint32_t a_lo = sw128_desc_lo(smem_u32(smem)), b_lo = sw128_desc_lo(smem_u32(smem) + F::kTokOff);
       const uint64_t s_lo = rows16_desc(smem_u32(smem) + F::kScaleOff);
@@ -748,9 +769,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int buf = static_cast<int>(count % kBufs);
           const uint32_t bpar = (count / kBufs) & 1u;
           ok = wait_phase(&tempty[buf], bpar ^ 1u, abort_flag, p);
+          const int cols = acc_cols(un.n);
+          if (ok && cols + before > F::kPool) {
+            // the unit before still holds columns of this one
+            ok = before > kTwoFit ? wait_phase(&tpart[buf ^ 1], (part_phase >> (buf ^ 1)) & 1u, abort_flag, p)
+                                  : wait_phase(&tempty[buf ^ 1], ((count - 1) / kBufs) & 1u, abort_flag, p);
+          }
+          if (cols > kTwoFit) part_phase ^= 1u << buf;
+          before = cols;
           tc_fence_after();
           const uint32_t id0 = idesc_mxf4(2 * kTileRows, un.n, 0), id1 = idesc_mxf4(2 * kTileRows, un.n, 1);
-          const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * F::NMAX);
+          const uint32_t dcol = tmem_base + acc_at<F>(buf, un.n);
           for (int kb = 0; ok && kb < KB; ++kb) {
             ok = wait_phase(&full[stage], phase, abort_flag, p);
             if (!ok) break;
@@ -867,57 +896,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!got_acc) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * F::NMAX);
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc_at<F>(buf, un.n);
       const int f0 = un.wb * kRowsPerWb + static_cast<int>(rank) * kCtaFeats;
       const int feat0 = f0 + 32 * (SWIGLU ? q & 1 : q);
-      if (feat0 < p.N) {
-        if constexpr (SWIGLU) {
-          // 32 tokens at a time: the gate warp keeps 0..15 and gives away
-          // 16..31, the up warp the other way round (columns past the run
-          // hold what they held; their rows are not stored)
-          const bool up = q >= 2;
-          for (int c = 32 * part; c < un.n; c += 32 * kEpiPer) {
-            uint32_t v[2][16];
-            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v[0]);
-            tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c + 16), v[1]);
-            tmem_ld_wait();
-            float4* give = xch + (2 * turn + (up ? 1 : 0)) * 128;
-            const float4* take = xch + (2 * turn + (up ? 0 : 1)) * 128;
-            float keep[16], got[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) keep[j] = __uint_as_float(up ? v[1][j] : v[0][j]);
-#pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              give[8 * j + lane] = make_float4(__uint_as_float(up ? v[0][j] : v[1][j]),
-                                               __uint_as_float(up ? v[0][j + 1] : v[1][j + 1]),
-                                               __uint_as_float(up ? v[0][j + 2] : v[1][j + 2]),
-                                               __uint_as_float(up ? v[0][j + 3] : v[1][j + 3]));
-            named_barrier(1 + wp, 64);
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 f = take[8 * j + lane];
-              got[j] = f.x;
-              got[j + 1] = f.y;
-              got[j + 2] = f.z;
-              got[j + 3] = f.w;
-            }
-            turn ^= 1;                   // the other buffer next: one barrier a block suffices
-            float gate[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              gate[j] = up ? got[j] : keep[j];
-              got[j] = up ? keep[j] : got[j];
-            }
-            emit_h16(p, un, feat0, up ? c + 16 : c, gate, got, lane);
-          }
-        } else {
-          for (int c = 16 * part; c < un.n; c += 16 * kEpiPer)
-            emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(c), stg, lane);
+      // Blocks of kBlock tokens.  An accumulator of more than kTwoFit columns
+      // is read in the order in which the next unit may need them, which takes
+      // up to NMAX from the pool's other end: from its last column down in
+      // place 0, from its first up in place 1; those that it may need are
+      // reported early.
+      constexpr int kBlock = SWIGLU ? 32 : 16;
+      const int cols = acc_cols(un.n);
+      int c = kBlock * part, step = kBlock * kEpiPer, left = (un.n - c + step - 1) / step, late = 0;
+      if (cols > kTwoFit) {
+        // blocks i < early of the order are reported early; this warp has every kEpiPer-th
+        const int early = (cols - (F::kPool - F::NMAX)) / kBlock;
+        late = left - (early - part + kEpiPer - 1) / kEpiPer;
+        if (buf == 0) {
+          c = (un.n - 1) / kBlock * kBlock - c;
+          step = -step;
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_leader + 8u * buf);
+#pragma unroll 1
+      for (;;) {
+        if (feat0 < p.N) {
+          for (; left > late; --left, c += step) {
+            if constexpr (SWIGLU) {
+              // The gate warp keeps tokens 0..15 and gives away 16..31, the up
+              // warp the other way round (columns past the run hold what they
+              // held; their rows are not stored).
+              const bool up = q >= 2;
+              uint32_t v[2][16];
+              tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v[0]);
+              tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c + 16), v[1]);
+              tmem_ld_wait();
+              float4* give = xch + (2 * turn + (up ? 1 : 0)) * 128;
+              const float4* take = xch + (2 * turn + (up ? 0 : 1)) * 128;
+              float keep[16], got[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) keep[j] = __uint_as_float(up ? v[1][j] : v[0][j]);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                give[8 * j + lane] = make_float4(__uint_as_float(up ? v[0][j] : v[1][j]),
+                                                 __uint_as_float(up ? v[0][j + 1] : v[1][j + 1]),
+                                                 __uint_as_float(up ? v[0][j + 2] : v[1][j + 2]),
+                                                 __uint_as_float(up ? v[0][j + 3] : v[1][j + 3]));
+              named_barrier(1 + wp, 64);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                const float4 f = take[8 * j + lane];
+                got[j] = f.x;
+                got[j + 1] = f.y;
+                got[j + 2] = f.z;
+                got[j + 3] = f.w;
+              }
+              turn ^= 1;                   // the other buffer next: one barrier a block suffices
+              float gate[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                gate[j] = up ? got[j] : keep[j];
+                got[j] = up ? keep[j] : got[j];
+              }
+              emit_h16(p, un, feat0, up ? c + 16 : c, gate, got, lane);
+            } else {
+              emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(c), stg, lane);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster((late ? tpart_leader : tempty_leader) + 8u * buf);
+        if (late == 0) break;
+        late = 0;
+      }
     }
   }
 

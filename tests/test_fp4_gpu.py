@@ -495,6 +495,31 @@ def test_as_many_experts_as_there_may_be(most):
     check_swiglu(codes, scales, g, g, size, size, K)
 
 
+@pytest.mark.parametrize("K", [64, 320])
+def test_accumulators_that_do_not_fit_side_by_side(K):
+    """Runs of 193 to 256 tokens next to one another and to short ones, several units for every pair of CTAs."""
+    rng = np.random.default_rng(K)
+    off = offsets_of([256, 250, 40, 230, 193, 256, 500, 17, 256])
+    E, rows, N = len(off) - 1, int(off[-1]), 4096
+    a, av = random_fp4(rng, 1, rows, K)
+    w, wv = random_fp4(rng, E, N, K)
+    ws = api.alloc_dispatch_workspace()
+    outs = [torch.empty(rows, N, dtype=t, device="cuda") for t in (torch.float32, torch.bfloat16)]
+    for out in outs:
+        api.moe_matmul_fp4(a, dev(off), w, out, ws)
+    h = api.fp4_empty(1, rows, N)
+    api.moe_swiglu_fp4(a, dev(off), w, w, h, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    codes, scales = ref.unpack(h[0].cpu().numpy())[0], ref.rows_of_scales(h[1].cpu().numpy(), N)[0]
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        want, size = av[0, r] @ wv[e].T, np.abs(av[0, r]) @ np.abs(wv[e]).T
+        add = (K / 64) * 2.0 ** -22 * size
+        for out in outs:
+            assert ref.within(out[r].double().cpu().numpy(), want, add + ref.half_step(out.dtype, np.abs(want) + add))
+        check_swiglu(codes[r], scales[r], want, want, size, size, K)
+
+
 def test_the_widest_rows():
     """K = 65,536, the longest accumulation: 256 stages for a unit."""
     rng = np.random.default_rng(2)
