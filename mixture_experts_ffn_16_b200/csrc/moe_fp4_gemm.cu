@@ -26,9 +26,9 @@
 //               chunks took 640-720 cycles a stage, more than the MMAs; loads
 //               to registers two stages ahead and 16-byte shared stores in
 //               their place made the products of large experts 13-20% slower.
-//   warps 4-11  epilogue: two warps per lane quarter.  A lane is a feature and
-//               a warp's 32 lanes are one block of h: its largest magnitude
-//               and the exchange of 8 x 8 codes are shuffles.  16 warps were
+//   warps 4-11  epilogue: two warps per lane quarter.  A lane of tensor memory
+//               is a feature, a warp's 32 lanes are one block of h, turned in
+//               shared memory to 8 features of a token a lane.  16 warps were
 //               slower (product 284 -> 315 us at 384 experts of 165 rows).
 //
 // What bounds them, on a B200 under its 1 kW limit (random operands; a plain
@@ -66,7 +66,9 @@ constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kBufs = 2;                                  // accumulators
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStgRow = 80;                               // 64 bytes of features + 16: distinct banks
-constexpr uint32_t kStgBytes = 16 * kStgRow;              // per epilogue warp
+constexpr uint32_t kXchTile = 16 * 32 * 4;                // 16 tokens x 32 features in fp32
+constexpr uint32_t kStgBytes = kXchTile;                  // per epilogue warp
+static_assert(16 * kStgRow <= kStgBytes, "staging of 16 tokens");
 constexpr int kSmemAlign = 1024;
 constexpr int kSmemTail = 512;                            // barriers, TMEM slot, abort flag
 constexpr int64_t kMaxUnits = 1 << 30;
@@ -235,86 +237,49 @@ __device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi) {
   }
 }
 
-// 8 lanes x 8 nibbles transposed: lane l of each group of 8 gives nibble t
-// for its feature and token t, and gets token l's nibbles of the 8 features.
-__device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane) {
-  uint32_t s = __shfl_xor_sync(0xffffffffu, w, 4);
-  w = (lane & 4) ? ((s >> 16) | (w & 0xFFFF0000u)) : ((w & 0x0000FFFFu) | (s << 16));
-  s = __shfl_xor_sync(0xffffffffu, w, 2);
-  w = (lane & 2) ? (((s >> 8) & 0x00FF00FFu) | (w & 0xFF00FF00u)) : ((w & 0x00FF00FFu) | ((s & 0x00FF00FFu) << 8));
-  s = __shfl_xor_sync(0xffffffffu, w, 1);
-  w = (lane & 1) ? (((s >> 4) & 0x0F0F0F0Fu) | (w & 0xF0F0F0F0u)) : ((w & 0x0F0F0F0Fu) | ((s & 0x0F0F0F0Fu) << 4));
-  return w;
-}
-
 // SiLU(g) u.  The result is rounded to 3 bits and a value next to a border
 // moves by a whole step, so the sigmoid is computed to a few fp32 ulps
 // (exponential and division of the special-function unit, not tanh.approx's
 // 2^-11).
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// h = SiLU(g) u of this lane's feature (feat0 + lane) for 16 tokens, as MXFP4:
-// the warp's 32 features are a block.  Stores the codes and scales of rows
-// un.row0 + c .. + 15 that belong to the run.  Two groups of 8 tokens side by
-// side, since the chain of one (special functions, exchanges) is latency.
-__device__ __forceinline__ void emit_h16(const Params& p, const Unit& un, int feat0, int c, const float (&g)[16],
-                                         const float (&u)[16], int lane) {
-  // Largest magnitude of each token over the lanes: three exchanges that halve
-  // the tokens a lane holds, two more; lanes 4 j .. 4 j + 3 end with token
-  // 8 o + j's.  (A warp reduction a token took 1440 cycles for 8 tokens where
-  // this takes 1110.)
-  float h[2][8];
-  uint32_t m[2][8], byte[2];
+// Words [16 tokens][32 features] of a warp's block in shared memory: written
+// by lane = feature, read 4 at a time by lane = (token, 8 features).  The xor
+// keeps the 8 lanes of such a read, 2 tokens, on distinct banks.
+__device__ __forceinline__ int xch_at(int tok, int feat) { return 32 * tok + (feat ^ (4 * (tok & 1))); }
+__device__ __forceinline__ void xch_get8(const float* x, int tok, int feat, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(x + xch_at(tok, feat));
+  const float4 b = *reinterpret_cast<const float4*>(x + xch_at(tok, feat + 4));
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// h of token `tok` of the run and features feat0 + 8 (lane & 3) .. + 7 as
+// MXFP4: the block's four lanes are neighbours.  (With a lane a feature and
+// the block's maximum by shuffles over 32 lanes, gate/up of 256 experts x 128
+// rows took 75 us.)
+__device__ __forceinline__ void emit_h8(const Params& p, const Unit& un, int feat0, int tok, const float (&h)[8],
+                                        int lane) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int o = 0; o < 2; ++o) {
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t byte = fp4_scale_byte(m);
+  const float inv = fp4_inv_scale(byte);
+  float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      h[o][j] = swiglu(g[8 * o + j], u[8 * o + j]);
-      m[o][j] = __float_as_uint(h[o][j]) & 0x7FFFFFFFu;
-    }
-  }
-#pragma unroll
-  for (int n = 4; n >= 1; n >>= 1) {
-    const bool hi = lane & (4 * n);
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-#pragma unroll
-      for (int j = 0; j < n; ++j) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, hi ? m[o][j] : m[o][j + n], 4 * n);
-        m[o][j] = max(hi ? m[o][j + n] : m[o][j], other);
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 0; o < 2; ++o) m[o][0] = max(m[o][0], __shfl_xor_sync(0xffffffffu, m[o][0], 2));
-#pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    m[o][0] = max(m[o][0], __shfl_xor_sync(0xffffffffu, m[o][0], 1));
-    byte[o] = fp4_scale_byte(m[o][0]);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      const float inv = __shfl_sync(0xffffffffu, fp4_inv_scale(byte[o]), 4 * j);
-      h[o][j] = inv == 0.0f ? 0.0f : h[o][j] * inv;
-    }
-  }
-  uint8_t* codes = static_cast<uint8_t*>(p.out) + static_cast<size_t>(un.row0 + c) * (p.N >> 1) + (feat0 >> 1);
-  uint8_t* scales = p.out_scales + (static_cast<size_t>(feat0 >> 7) * p.rows + un.row0 + c) * 4 + ((feat0 >> 5) & 3);
-  uint32_t w[2];
-#pragma unroll
-  for (int o = 0; o < 2; ++o) w[o] = transpose_nibbles(e2m1x8(h[o]), lane);
-#pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    const int tok = 8 * o + (lane & 7), stok = 8 * o + (lane >> 2);
-    if (c + tok < un.rows)
-      *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(tok) * (p.N >> 1) + 4 * (lane >> 3)) = w[o];
-    if ((lane & 3) == 0 && c + stok < un.rows) {
-      scales[4 * stok] = static_cast<uint8_t>(byte[o]);
-      // f a multiple of 64 only: the last word's two spare bytes
-      if (feat0 + 32 == p.N && (p.N & 127)) *reinterpret_cast<uint16_t*>(scales + 4 * stok + 1) = 0;
-    }
+  for (int j = 0; j < 8; ++j) v[j] = h[j] * inv;
+  const uint32_t word = byte == kFp4NanScale ? 0u : e2m1x8(v);
+  if (tok >= un.rows) return;
+  const size_t row = static_cast<size_t>(un.row0) + tok;
+  uint8_t* codes = static_cast<uint8_t*>(p.out) + row * (p.N >> 1) + (feat0 >> 1);
+  *reinterpret_cast<uint32_t*>(codes + 4 * (lane & 3)) = word;
+  if ((lane & 3) == 0) {
+    uint8_t* scale = p.out_scales + (static_cast<size_t>(feat0 >> 7) * p.rows + row) * 4 + ((feat0 >> 5) & 3);
+    *scale = static_cast<uint8_t>(byte);
+    // f a multiple of 64 only: the last word's two spare bytes
+    if (feat0 + 32 == p.N && (p.N & 127)) *reinterpret_cast<uint16_t*>(scale + 1) = 0;
   }
 }
 
@@ -593,13 +558,18 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), g);
             tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(F::NMAX + c), v);
             tmem_ld_wait();
-            float gate[16], up[16];
+            float* x = reinterpret_cast<float*>(stg);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              gate[j] = __uint_as_float(g[j]);
-              up[j] = __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j)
+              x[xch_at(j, lane)] = swiglu(__uint_as_float(g[j]), __uint_as_float(v[j]));
+            __syncwarp();
+#pragma unroll
+            for (int o = 0; o < 16; o += 8) {
+              float h[8];
+              xch_get8(x, o + (lane >> 2), 8 * (lane & 3), h);
+              emit_h8(p, un, feat0, c + o + (lane >> 2), h, lane);
             }
-            emit_h16(p, un, feat0, c, gate, up, lane);
+            __syncwarp();
           }
         }
       } else {
@@ -639,15 +609,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 //   product: CTA r has output features 128 r .. of the unit's 256.
 //   swiglu:  CTA r has features 64 r .. of the unit's 128, their gate rows in
 //            lanes 0..63 and their up rows in lanes 64..127.  A gate warp and
-//            the up warp of the same features exchange half of their values
-//            through shared memory, then each finishes 16 of 32 tokens.
+//            the up warp of the same features put 16 tokens of both into shared
+//            memory, then each finishes 8 of them.
 // Roles as above, in both CTAs; the MMAs are issued by the leader (rank 0)
 // for both.  cp.async can only arrive on a barrier of its own CTA, so the
 // peer's scale copies complete a barrier there, and the peer's warp 1, which
 // has no MMAs to issue, reports it to the leader's.  (A scale warp that waited
 // for its own copies and reported them itself took 1.35 us a stage: its
 // cluster-scope release waits for the copies of later stages too.)
-constexpr uint32_t kXchBytes = 2 * 2 * 32 * 16 * 4;       // per warp pair: 2 buffers x 2 directions x 32 lanes x 16 floats
+constexpr uint32_t kXchBytes = 2 * 2 * kXchTile;          // per warp pair: 2 buffers of gate and up
 
 using Pair = Form<1, 256, 128, 5, kEpiWarps / 2 * kXchBytes>;
 
@@ -877,7 +847,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint8_t* stg = stg_all + (warp - kFirstEpi) * kStgBytes;
     // swiglu: lane quarters q and q ^ 2 hold gate and up of the same features
     const int wp = 2 * part + (q & 1);
-    float4* xch = reinterpret_cast<float4*>(stg_all + wp * kXchBytes);
+    float* xch = reinterpret_cast<float*>(stg_all + wp * kXchBytes);
     volatile int* vote = reinterpret_cast<volatile int*>(wsum + kThreads / 32) + 2 * wp;
     uint32_t count = 0;
     int turn = 0;
@@ -904,7 +874,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // up to NMAX from the pool's other end: from its last column down in
       // place 0, from its first up in place 1; those that it may need are
       // reported early.
-      constexpr int kBlock = SWIGLU ? 32 : 16;
+      constexpr int kBlock = 16;
       const int cols = acc_cols(un.n);
       int c = kBlock * part, step = kBlock * kEpiPer, left = (un.n - c + step - 1) / step, late = 0;
       if (cols > kTwoFit) {
@@ -921,42 +891,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (feat0 < p.N) {
           for (; left > late; --left, c += step) {
             if constexpr (SWIGLU) {
-              // The gate warp keeps tokens 0..15 and gives away 16..31, the up
-              // warp the other way round (columns past the run hold what they
-              // held; their rows are not stored).
-              const bool up = q >= 2;
-              uint32_t v[2][16];
-              tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v[0]);
-              tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c + 16), v[1]);
+              // gate and up of 16 tokens meet in shared memory, each warp
+              // finishes 8 of them
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(tb + static_cast<uint32_t>(c), v);
               tmem_ld_wait();
-              float4* give = xch + (2 * turn + (up ? 1 : 0)) * 128;
-              const float4* take = xch + (2 * turn + (up ? 0 : 1)) * 128;
-              float keep[16], got[16];
+              float* x = xch + turn * (kXchTile / 2);
+              float* mine = x + (q >> 1) * (kXchTile / 4);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) keep[j] = __uint_as_float(up ? v[1][j] : v[0][j]);
-#pragma unroll
-              for (int j = 0; j < 16; j += 4)
-                give[8 * j + lane] = make_float4(__uint_as_float(up ? v[0][j] : v[1][j]),
-                                                 __uint_as_float(up ? v[0][j + 1] : v[1][j + 1]),
-                                                 __uint_as_float(up ? v[0][j + 2] : v[1][j + 2]),
-                                                 __uint_as_float(up ? v[0][j + 3] : v[1][j + 3]));
+              for (int j = 0; j < 16; ++j) mine[xch_at(j, lane)] = __uint_as_float(v[j]);
               named_barrier(1 + wp, 64);
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 f = take[8 * j + lane];
-                got[j] = f.x;
-                got[j + 1] = f.y;
-                got[j + 2] = f.z;
-                got[j + 3] = f.w;
-              }
               turn ^= 1;                   // the other buffer next: one barrier a block suffices
-              float gate[16];
+              const int tok = 8 * (q >> 1) + (lane >> 2);
+              float g[8], h[8];
+              xch_get8(x, tok, 8 * (lane & 3), g);
+              xch_get8(x + kXchTile / 4, tok, 8 * (lane & 3), h);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                gate[j] = up ? got[j] : keep[j];
-                got[j] = up ? keep[j] : got[j];
-              }
-              emit_h16(p, un, feat0, up ? c + 16 : c, gate, got, lane);
+              for (int j = 0; j < 8; ++j) h[j] = swiglu(g[j], h[j]);
+              emit_h8(p, un, feat0, c + tok, h, lane);
             } else {
               emit_out16<KIND>(p, un, feat0, c, tb + static_cast<uint32_t>(c), stg, lane);
             }
