@@ -35,11 +35,12 @@
 // copy of random data draws 0.88-0.97 kW there, 148 pJ a byte of HBM traffic):
 // experts of few rows stream their weights at the copy bandwidth (512 experts,
 // 640 rows, N = 4096, K = 1024: 115 us, 7.0 TB/s).  With many rows the power
-// limit binds: 64 experts x 512 rows, N = K = 4096 takes 350 us (3.1 PFLOP/s,
-// 1.37 GHz), of which the MMAs alone, on operands that are already there, take
-// 175 us at 0.99 kW and everything else without them 270 us at 0.99 kW.  Fewer
-// cycles (a look at the next stage's barrier during the MMAs) changed nothing.
-// DRAM reads are the operands once (164 MB of 160 at 16 experts x 512 rows).
+// limit binds: 64 experts x about 512 rows, N = K = 4096 takes 340 us (3.2
+// PFLOP/s, 1.4 GHz).  The MMAs alone, on operands that are already there, take
+// 175 us of the 1 kW, the tensor loads alone 184 us, loads and epilogue 245 us;
+// without the scales' copies to shared memory it takes 331 us, without those to
+// tensor memory 323 us.  The clock takes what is saved, up to 1.9 GHz.  DRAM
+// reads are the operands once (166 MB of 160 at 16 experts x 512 rows).
 //
 // K need not be a multiple of 256: loads past its end read zeros, and the MMAs
 // past it are not issued.
@@ -832,7 +833,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) cp_async_4(dst + h * kChunkScales + 4 * c, wsrc[c] + static_cast<size_t>(kc) * p.N);
 #pragma unroll
         for (int c = 0; c < 4 * F::NB; ++c)
-          if (32 * c < un.n) cp_async_4(dst + (2 * F::NA + F::NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
+          if (32 * c < un.n)
+            cp_async_4(dst + (2 * F::NA + F::NB * h + c / 4) * kChunkScales + 4 * (c & 3), tsrc + trow[c]);
         cp_async_mbar_arrive_noinc(&full[stage]);
         if (++stage == S) {
           stage = 0;
