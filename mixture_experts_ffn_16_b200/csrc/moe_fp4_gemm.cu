@@ -968,11 +968,12 @@ int launch_kind(const Params& prm, bool pair, int sms, cudaStream_t st) {
 
 int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err, cudaStream_t st) {
   const bool swiglu = q.w1_codes != nullptr;
-  // CTA pairs above 96 rows an expert, what a single CTA's unit takes in one
-  // run.  64 experts of 104 / 128 / 160 / 512 rows, pairs against single CTAs:
-  // N = 4096, K = 1024 product 38 / 43 / 47 / 123 us against 43 / 48 / 52 / 142;
-  // f = 1024, K = 4096 gate/up 60 / 64 / 70 / 186 against 66 / 71 / 75 / 210.
-  // 256 experts of 96 / 64 rows: 259 / 240 against 241 / 203 (gate/up).
+  // CTA pairs above 96 rows an expert on average, what a single CTA's unit
+  // takes in one run.  64 experts of 96 / 104 / 128 / 512 rows, pairs against
+  // single CTAs: N = 4096, K = 1024 product 39 / 39 / 42 / 121 us against 34 /
+  // 44 / 46 / 146; f = 1024, K = 4096 gate/up 59 / 61 / 64 / 170 against 55 /
+  // 66 / 68 / 211.  256 experts of 96 rows on average, the largest 48 times the
+  // smallest: gate/up 259 against 244.
   const int64_t avg = (static_cast<int64_t>(q.rows) + q.E - 1) / q.E;
   const bool pair = avg > Single::NMAX && di.sms >= 2;
   Params p;
