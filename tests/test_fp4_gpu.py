@@ -520,6 +520,29 @@ def test_accumulators_that_do_not_fit_side_by_side(K):
         check_swiglu(codes[r], scales[r], want, want, size, size, K)
 
 
+@pytest.mark.parametrize("K", [64, 512])
+def test_products_repeat_bitwise(K):
+    """Thirty runs of each product over runs of all lengths, on CTA pairs and on single CTAs, into cleared outputs."""
+    rng = np.random.default_rng(K + 1)
+    for counts in (rng.integers(0, 400, 60), rng.integers(0, 150, 120)):
+        off = dev(offsets_of(counts))
+        E, rows, N = len(counts), int(counts.sum()), 2048
+        a, _ = random_fp4(rng, 1, rows, K)
+        w, _ = random_fp4(rng, E, N, K)
+        ws = api.alloc_dispatch_workspace()
+        out, h = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda"), api.fp4_empty(1, rows, N)
+        first = None
+        for _ in range(30):
+            for t in (out, *h):
+                t.zero_()
+            api.moe_matmul_fp4(a, off, w, out, ws)
+            api.moe_swiglu_fp4(a, off, w, w, h, ws)
+            got = [t.clone() for t in (out, *h)]
+            first = first or got
+            assert all(torch.equal(p, q) for p, q in zip(first, got))
+        assert api.moe_device_status(ws) == api.MOE_OK
+
+
 def test_the_widest_rows():
     """K = 65,536, the longest accumulation: 256 stages for a unit."""
     rng = np.random.default_rng(2)
