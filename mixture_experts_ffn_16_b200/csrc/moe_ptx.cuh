@@ -41,6 +41,13 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// 1 / x to an ulp or so; 0 where that is subnormal.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

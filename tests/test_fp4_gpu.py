@@ -579,3 +579,99 @@ def test_the_most_rows():
         want = wv[np.searchsorted(off, r, side="right") - 1] @ x
         assert ref.within(out[r].double().cpu().numpy(), want, ref.half_step(out.dtype, want) + 2.0 ** -22 * 64 * 36)
     assert not bool(out[rows - 2:].any())
+
+
+def weight_row(value, blocks):
+    """Codes and scale bytes [blocks] whose first elements add up to `value`, 2 bits or more a block (greedy)."""
+    code, byte = np.zeros(blocks, dtype=int), np.full(blocks, 127)
+    left = float(value)
+    for i in range(blocks):
+        if left == 0.0:
+            break
+        m, e = np.frexp(abs(left))                       # 0.5 <= m < 1: the nearest of 0.5, 0.75 and 1
+        near = (0.5, 0.75, 1.0)[int(np.argmin([abs(m - 0.5), abs(m - 0.75), abs(m - 1.0)]))]
+        four = int(near * 8)                             # 4 or 6 (code 6, 7) times 2^(e - 3); 8 is 4 times 2^(e - 2)
+        up = int(four == 8)
+        byte[i] = 127 + e - 3 + up
+        code[i] = (7 if four == 6 else 6) + (8 if left < 0 else 0)
+        left -= np.sign(left) * np.ldexp(near, int(e))
+    return code, byte
+
+
+def swiglu_of(g, u, counts):
+    """h codes and scale bytes [rows, f] of gate sums g and up sums u [f], the same in every row, and the sums there were."""
+    f, blocks = len(g), 16
+    K = 32 * blocks
+    off = offsets_of(counts)
+    E, rows = len(counts), int(off[-1])
+    one = np.zeros((1, rows, K), dtype=int)
+    one[..., ::32] = 2                                   # 1.0 in the first element of every block
+    a = tuple(map(dev, ref.pack(one, np.full((1, rows, blocks), 127))))
+    weights, sums = [], []
+    for target in (g, u):
+        code, byte = np.zeros((E, f, K), dtype=int), np.empty((E, f, blocks), dtype=int)
+        for j in range(f):
+            c, b = weight_row(target[j], blocks)
+            code[:, j, ::32], byte[:, j] = c, b
+        pair = ref.pack(code, byte)
+        weights.append(tuple(map(dev, pair)))
+        sums.append(ref.dequantize(*pair)[0].sum(-1))
+    h, ws = api.fp4_empty(1, rows, f), api.alloc_dispatch_workspace()
+    api.moe_swiglu_fp4(a, dev(off), *weights, h, ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    return ref.unpack(h[0].cpu().numpy())[0], ref.rows_of_scales(h[1].cpu().numpy(), f)[0], *sums
+
+
+FORMS = [[3], [200, 120]]                                # single CTAs, CTA pairs
+
+
+@pytest.mark.parametrize("counts", FORMS)
+@pytest.mark.parametrize("gate", [-88.6, -87.5, -86.0, -80.0, -60.0, -40.0, -20.0, -8.0, -1.0, 0.5, 3.0, 20.0])
+def test_swiglu_beside_the_borders(gate, counts):
+    """Values of h a few ulps to either side of the borders between codes, at gates far from zero: the right code.
+
+    In units of 2^-24 of the value: expf 4 (2 ulps), the sum 1, the quotient 1, the product 1, so 7 in all.  Values
+    lie 8 or more from a border.  Feature 0 of each block of 32 is 4, so the block's scale is 1."""
+    rng = np.random.default_rng(int(-gate * 10) % 1000)
+    f = 64
+    g = np.float32(gate) * (1 + rng.random(f) / 200)
+    g = np.round(np.maximum(g, -88.7) * 2.0 ** 14) / 2.0 ** 14       # 21 bits
+    silu = lambda x: x * np.exp(-np.logaddexp(0.0, -x))
+    border = rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], f)
+    side = rng.choice([-1.0, 1.0], f)
+    u = border * (1 + side * 12 * 2.0 ** -24) / silu(g)
+    m, e = np.frexp(u)
+    u = np.ldexp(np.round(m * 2.0 ** 22), e - 22)        # 22 bits: every partial sum of the product is exact
+    g[::32], u[::32] = 64.0, 2.0 ** -4
+    codes, scales, g, u = swiglu_of(g, u, counts)
+    h = silu(g) * u
+    edges = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    gap = np.abs(np.abs(h)[:, None] / edges - 1).min(1) * 2.0 ** 24
+    sure = gap >= 8                                      # rounding u to 22 bits brought some of them nearer
+    assert sure.sum() >= f // 2 and (gap[sure] <= 40).sum() >= f // 3
+    want = (np.abs(h)[:, None] > edges).sum(1)
+    assert (scales == 127).all()
+    assert np.array_equal((codes & 7)[:, sure], np.tile(want[sure], (len(codes), 1)))
+    assert np.array_equal((codes >> 3)[:, sure], np.tile((h < 0)[sure], (len(codes), 1)))
+
+
+@pytest.mark.parametrize("counts", FORMS)
+def test_swiglu_at_the_ends_of_fp32(counts):
+    """A product g u past fp32 makes its block NaN and no other; gates past the exponential's range give 0 or g u."""
+    big = 2.0 ** 100
+    g, u = np.full(192, 1.0), np.full(192, 1.0)
+    g[3], u[3] = big, big                                # block 0: +inf
+    g[40], u[40] = big, -big                             # block 1: -inf
+    g[64:96], u[64:96] = -89.0 - np.arange(32), 2.0      # block 2: all of it 0 (|SiLU| below 2.6e-37 and flushed)
+    g[96:128], u[96:128] = -1.5 * 2.0 ** 126, big        # block 3: 0
+    g[128:160], u[128:160] = 1.5 * 2.0 ** 124, 2.0 ** -124        # block 4: SiLU(g) = g, h = 1.5
+    g[160:], u[160:] = 0.0, big                          # block 5: 0
+    codes, scales, _, _ = swiglu_of(g, u, counts)
+    silu1 = 1.0 / (1.0 + np.exp(-1.0))                   # 0.731: scale 2^(-1 - 2), 5.85 rounds to 6
+    assert (scales[:, :2] == 255).all() and not codes[:, :64].any()
+    assert (scales[:, 2:4] == 0).all() and not (codes[:, 64:128] & 7).any()
+    assert (scales[:, 4] == 125).all() and (codes[:, 128:160] == 7).all()
+    assert (scales[:, 5] == 0).all() and not (codes[:, 160:] & 7).any()
+    g[3] = u[3] = g[40] = u[40] = 1.0
+    codes, scales, _, _ = swiglu_of(g, u, counts)
+    assert silu1 * 8 > 5 and (scales[:, :2] == 124).all() and (codes[:, :64] == 7).all()
