@@ -188,14 +188,19 @@ __device__ __forceinline__ Unit find_unit(const int* first, const int* off, int 
 }
 
 // Bounded wait for a barrier phase: the thread sleeps in the hardware, up to
-// 20 us an attempt.  The clock is read every 8 attempts only.
+// 20 us an attempt.  The clock is read every 8 attempts only.  CLUSTER: the
+// peer CTA's threads arrive too, with a release at cluster scope.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                            const Params& p) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait(a, parity)) return true;
+  const auto arrived = [&] {
+    return CLUSTER ? mbar_try_wait_sleep_cluster(a, parity, 20000u) : mbar_try_wait_sleep(a, parity, 20000u);
+  };
+  if (CLUSTER ? arrived() : mbar_try_wait(a, parity)) return true;
   int64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_sleep(a, parity, 20000u)) return true;
+    if (arrived()) return true;
     if ((it & 7u) == 0) {
       if (*abort_flag) return false;
       const int64_t now = clock64();
@@ -627,9 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 // Roles as above, in both CTAs; the MMAs are issued by the leader (rank 0)
 // for both.  cp.async can only arrive on a barrier of its own CTA, so the
 // peer's scale copies complete a barrier there, and the peer's warp 1, which
-// has no MMAs to issue, reports it to the leader's.  (A scale warp that waited
-// for its own copies and reported them itself took 1.35 us a stage: its
-// cluster-scope release waits for the copies of later stages too.)
+// has no MMAs to issue, reports it to the leader's, with a release restricted to
+// shared memory.  (With a full release at cluster scope 64 experts x about 512
+// rows, N = K = 4096, took 838 us in place of 304, a prefill of 4096 tokens on
+// 256 experts 266 in place of 149.)
 constexpr uint32_t kXchBytes = 2 * 2 * kXchTile;          // per warp pair: 2 buffers of gate and up
 
 using Pair = Form<1, 256, 128, 5, kEpiWarps / 2 * kXchBytes>;
@@ -764,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t id0 = idesc_mxf4(2 * kTileRows, un.n, 0), id1 = idesc_mxf4(2 * kTileRows, un.n, 1);
           const uint32_t dcol = tmem_base + acc_at<F>(buf, un.n);
           for (int kb = 0; ok && kb < KB; ++kb) {
-            ok = wait_phase(&full[stage], phase, abort_flag, p);
+            ok = wait_phase<true>(&full[stage], phase, abort_flag, p);
             if (!ok) break;
             tc_fence_after();
             fence_proxy_async_smem();
@@ -800,12 +806,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < KB; ++kb) {
             ok = wait_phase(&full[stage], phase, abort_flag, p);
             if (!ok) break;
-            // The scales are in this CTA's shared memory and only its own
-            // tensor core reads them, once the leader has seen this arrival:
-            // ordered by the proxy fence, no cluster-scope release (which
-            // cost half of the rate).
+            // The scales, written by asynchronous copies to this CTA's shared
+            // memory, are read by its tensor core at the leader's request:
+            // proxy fence, then release at cluster scope, which the leader's
+            // wait acquires.
             fence_proxy_async_smem();
-            mbar_arrive_cluster(full_leader + 8u * stage);
+            mbar_arrive_cluster_release_smem(full_leader + 8u * stage);
             if (++stage == S) {
               stage = 0;
               phase ^= 1u;

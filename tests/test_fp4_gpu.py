@@ -675,3 +675,37 @@ def test_swiglu_at_the_ends_of_fp32(counts):
     g[3] = u[3] = g[40] = u[40] = 1.0
     codes, scales, _, _ = swiglu_of(g, u, counts)
     assert silu1 * 8 > 5 and (scales[:, :2] == 124).all() and (codes[:, :64] == 7).all()
+
+
+@pytest.mark.parametrize("N,K", [(512, 256), (2048, 1024), (1024, 2112)])
+def test_scales_of_the_run_are_the_ones_used(N, K):
+    """Two sets of inputs of one shape, whose scales differ by 2^16 and more, in turn: a scale left in shared or tensor
+    memory by the call or the stage before would show.  On CTA pairs, each of whose CTAs copies its own scales."""
+    rng = np.random.default_rng(N)
+    off_host = offsets_of([130, 97, 256, 0, 301])
+    off, E, rows = dev(off_host), len(off_host) - 1, int(off_host[-1])
+    sets, ws = [], api.alloc_dispatch_workspace()
+    for shift in (0, 24):
+        a, av = random_fp4(rng, 1, rows, K, spread=2)
+        w, wv = random_fp4(rng, E, N, K, spread=2)
+        a[1].add_(shift)
+        w[1].sub_(shift // 3)
+        out, h = torch.zeros(rows, N, device="cuda"), api.fp4_empty(1, rows, N)
+        up = (w[0], w[1] - (8 + shift))                  # keeps h finite
+        api.moe_matmul_fp4(a, off, w, out, ws)
+        api.moe_swiglu_fp4(a, off, w, up, h, ws)
+        for e in range(E):
+            r = slice(off_host[e], off_host[e + 1])
+            scale = 2.0 ** (shift - shift // 3)
+            want, size = av[0, r] @ wv[e].T * scale, np.abs(av[0, r]) @ np.abs(wv[e]).T * scale
+            add = (K / 64) * 2.0 ** -22 * size
+            assert ref.within(out[r].double().cpu().numpy(), want, add + ref.half_step(out.dtype, np.abs(want) + add))
+        sets.append((a, w, up, out, h, [t.clone() for t in (out, *h)]))
+    for _ in range(60):
+        for a, w, up, out, h, first in sets:
+            for t in (out, *h):
+                t.zero_()
+            api.moe_matmul_fp4(a, off, w, out, ws)
+            api.moe_swiglu_fp4(a, off, w, up, h, ws)
+            assert all(torch.equal(p, q) for p, q in zip(first, (out, *h)))
+    assert api.moe_device_status(ws) == api.MOE_OK
