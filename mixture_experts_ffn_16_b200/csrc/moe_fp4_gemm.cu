@@ -757,12 +757,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           const int buf = static_cast<int>(count % kBufs);
           const uint32_t bpar = (count / kBufs) & 1u;
-          ok = wait_phase(&tempty[buf], bpar ^ 1u, abort_flag, p);
+          ok = wait_phase<true>(&tempty[buf], bpar ^ 1u, abort_flag, p);
           const int cols = acc_cols(un.n);
           if (ok && cols + before > F::kPool) {
             // the unit before still holds columns of this one
-            ok = before > kTwoFit ? wait_phase(&tpart[buf ^ 1], (part_phase >> (buf ^ 1)) & 1u, abort_flag, p)
-                                  : wait_phase(&tempty[buf ^ 1], ((count - 1) / kBufs) & 1u, abort_flag, p);
+            ok = before > kTwoFit ? wait_phase<true>(&tpart[buf ^ 1], (part_phase >> (buf ^ 1)) & 1u, abort_flag, p)
+                                  : wait_phase<true>(&tempty[buf ^ 1], ((count - 1) / kBufs) & 1u, abort_flag, p);
           }
           if (cols > kTwoFit) part_phase ^= 1u << buf;
           before = cols;
@@ -936,7 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster((late ? tpart_leader : tempty_leader) + 8u * buf);
+        if (lane == 0) mbar_arrive_cluster_relaxed((late ? tpart_leader : tempty_leader) + 8u * buf);
         if (late == 0) break;
         late = 0;
       }

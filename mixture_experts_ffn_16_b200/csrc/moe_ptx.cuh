@@ -295,9 +295,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same for shared memory of this CTA that must be visible to the thread of
-// the peer CTA which waits for the arrival with acquire at cluster scope (and
-// to what that thread orders behind it).  The release is a fence restricted to
+// The same at cluster scope, without a release: for tensor memory handed back
+// between tcgen05.fence::before_thread_sync here and a wait at cluster scope with
+// tcgen05.fence::after_thread_sync there, which is all the order it needs.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// An arrival that makes this CTA's shared memory visible to the thread of the
+// peer CTA which waits for it with acquire at cluster scope (and to what that
+// thread orders behind it).  The release is a fence restricted to
 // this CTA's shared memory: a full release at cluster scope also waits for the
 // CTA's outstanding accesses to global memory, 0.7-1.4 us each.
 __device__ __forceinline__ void mbar_arrive_cluster_release_smem(uint32_t cluster_addr) {
