@@ -224,12 +224,11 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, const
   }
 }
 
-// One lane waits, the warp learns the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int lane, volatile int* abort_flag,
-                                          const Params& p) {
-  int got = 1;
-  if (lane == 0) got = wait_phase(bar, parity, abort_flag, p) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, got, 0) != 0;
+// Every lane waits, since each goes on to touch what the barrier guards (a
+// shuffle from one that waits would not order the others' accesses); all or
+// none go on.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const Params& p) {
+  return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p));
 }
 
 template <int KIND>
@@ -530,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 #pragma unroll
       for (int c = 0; c < 4 * F::NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
       for (int kb = 0; kb < KB; ++kb) {
-        ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
+        ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, p);
         if (!ok) break;
         const uint32_t dst = smem_u32(smem + stage * F::kStage) + F::kScaleOff + 16u * lane;
         const int kc = min(2 * kb + h, KC - 1);
@@ -563,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
       const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int buf = static_cast<int>(count % kBufs);
       const uint32_t bpar = (count / kBufs) & 1u;
-      if (!warp_wait(&tfull[buf], bpar, lane, abort_flag, p)) break;
+      if (!warp_wait(&tfull[buf], bpar, abort_flag, p)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                           static_cast<uint32_t>(buf * F::NA * F::NMAX);
@@ -842,7 +841,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4 * F::NB; ++c) trow[c] = static_cast<uint32_t>(min(un.row0 + 32 * c + lane, p.rows - 1));
       for (int kb = 0; kb < KB; ++kb) {
-        ok = warp_wait(&empty[stage], phase ^ 1u, lane, abort_flag, p);
+        ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, p);
         if (!ok) break;
         const uint32_t dst = smem_u32(smem + stage * F::kStage) + F::kScaleOff + 16u * lane;
         const int kc = min(2 * kb + h, KC - 1);
@@ -875,7 +874,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit un = find_unit<F>(first, off, p.E, u, lane);
       const int buf = static_cast<int>(count % kBufs);
       const uint32_t bpar = (count / kBufs) & 1u;
-      bool got_acc = warp_wait(&tfull[buf], bpar, lane, abort_flag, p);
+      bool got_acc = warp_wait(&tfull[buf], bpar, abort_flag, p);
       if constexpr (SWIGLU) {
         // Both warps of an exchange go on, or neither does: they meet at its
         // barriers.  The slots of a unit are written again two units later.
