@@ -9,9 +9,13 @@ CUDA kernels; there is no CPU path, and a missing library raises at load time.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
+
+from . import build as _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -150,7 +154,9 @@ def _fast():
     global _fastcall
     if _fastcall is None:
         lib = load()
-        from . import _fastcall as native
+        loader = importlib.machinery.ExtensionFileLoader(__package__ + "._fastcall", _build.fastcall_path())
+        native = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(native)
         native.bind(tuple(ctypes.cast(getattr(lib, "moe_" + n), ctypes.c_void_p).value for n in _FAST_CALLS))
         _fastcall = native
     return _fastcall

@@ -1,9 +1,10 @@
 """Build libmoe.so in-tree: every .cu under csrc/ compiled for sm_100a with nvcc
 and linked into one shared library (CUDA runtime linked statically, so the
 library loads on a machine without a GPU driver; it needs the driver only
-when a kernel is launched).  And _fastcall.so, the Python binding's native
-part (csrc/fastcall.cpp), compiled with the host compiler against torch's
-headers; torch's libraries are in the process when it is imported."""
+when a kernel is launched).  And, where there is torch, the Python binding's
+native part (csrc/fastcall.cpp), compiled with the host compiler against
+torch's headers, whose layout of tensors it takes over: the file's name says
+which torch and which Python it is for, and no other loads it."""
 from __future__ import annotations
 
 import os
@@ -14,7 +15,6 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
-FAST = os.path.join(HERE, "_fastcall.so")
 BUILD = os.path.join(HERE, "_build")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
@@ -44,14 +44,22 @@ def up_to_date():
     return _newer(LIB, _deps())
 
 
-def build_fastcall(force: bool = False, verbose: bool = False) -> str:
-    src = os.path.join(CSRC, "fastcall.cpp")
-    if not force and _newer(FAST, [src, os.path.join(INCLUDE, "moe.h")]):
-        return FAST
+def fastcall_path() -> str:
+    """Where the binding's native part for this torch and this Python is, or would be."""
     import torch
+    abi = f"torch-{torch.__version__}-cxx11abi{int(torch.compiled_with_cxx11_abi())}"
+    return os.path.join(HERE, f"_fastcall-{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def build_fastcall(force: bool = False, verbose: bool = False) -> str:
+    import torch
+    out = fastcall_path()
+    src = os.path.join(CSRC, "fastcall.cpp")
+    if not force and _newer(out, [src, os.path.join(INCLUDE, "moe.h")]):
+        return out
     inc, libs = (os.path.join(os.path.dirname(torch.__file__), d) for d in ("include", "lib"))
     cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
-    tmp = FAST + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
@@ -60,8 +68,8 @@ def build_fastcall(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, FAST)
-    return FAST
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

@@ -1,10 +1,15 @@
 """The native part of the binding: plain calls are its own and do what the Python part does; all else it leaves."""
+import os
+import subprocess
+import sys
+import sysconfig
+
 import numpy as np
 import pytest
 import torch
 
 import fp4_ref as ref
-from mixture_experts_ffn_16_b200 import api
+from mixture_experts_ffn_16_b200 import api, build
 
 T, K, E, D, F = 37, 3, 5, 192, 128
 NAMES = ["sort_tokens", "dispatch", "dispatch_backward", "undispatch", "undispatch_backward", "quantize_fp4",
@@ -147,3 +152,26 @@ def test_leaves_wrong_tensors_to_the_python_part(name):
     getattr(api, "moe_" + name)(*sub)
     torch.cuda.synchronize()
     assert any(o.any() for o in outs)
+
+
+def test_file_of_the_native_part_says_what_it_was_compiled_for(monkeypatch, tmp_path):
+    """Another torch or Python has another file: what was built for one is neither kept nor loaded for the other."""
+    here = build.build_fastcall()
+    assert here == build.fastcall_path() and os.path.exists(here)
+    assert torch.__version__ in here and here.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert api._fast().__file__ == here
+    made = []
+
+    def compiler(cmd):
+        made.append(cmd[cmd.index("-o") + 1])
+        open(made[-1], "w").close()
+
+    monkeypatch.setattr(build, "HERE", str(tmp_path))
+    monkeypatch.setattr(subprocess, "check_call", compiler)
+    first = build.build_fastcall()
+    assert len(made) == 1 and build.build_fastcall() == first and len(made) == 1
+    monkeypatch.setattr(torch, "__version__", "2.99.0+cu999")
+    second = build.build_fastcall()
+    assert second != first and len(made) == 2
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-none.so")
+    assert build.build_fastcall() not in (first, second) and len(made) == 3
