@@ -12,6 +12,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -149,14 +150,27 @@ def load():
     return lib
 
 
+class _NoFast:
+    """In place of the native part where it has not been built for this torch and Python: makes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _fast():
     """The native part of the binding (csrc/fastcall.cpp), given the library's addresses once."""
     global _fastcall
     if _fastcall is None:
         lib = load()
         loader = importlib.machinery.ExtensionFileLoader(__package__ + "._fastcall", _build.fastcall_path())
-        native = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
-        loader.exec_module(native)
+        try:
+            native = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+            loader.exec_module(native)
+        except ImportError as e:
+            warnings.warn(f"token-dispatch and MXFP4 calls go through ctypes, 3 us of host time more each, until "
+                          f"`python -m {__package__}.build` has built their native part: {e}")
+            _fastcall = _NoFast()
+            return _fastcall
         native.bind(tuple(ctypes.cast(getattr(lib, "moe_" + n), ctypes.c_void_p).value for n in _FAST_CALLS))
         _fastcall = native
     return _fastcall

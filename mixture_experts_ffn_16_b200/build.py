@@ -11,6 +11,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -73,7 +74,19 @@ def build_fastcall(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    build_fastcall(force, verbose)
+    """The library, then the binding's native part.  The library needs neither torch nor that part, and the binding
+    does without it: where it cannot be built there is a warning, and without torch nothing."""
+    lib = build_library(force, verbose, ptxas_info)
+    try:
+        build_fastcall(force, verbose)
+    except ImportError:
+        pass
+    except (OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"the binding's native part was not built, its calls will go through ctypes: {e}")
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -175,3 +175,51 @@ def test_file_of_the_native_part_says_what_it_was_compiled_for(monkeypatch, tmp_
     assert second != first and len(made) == 2
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-none.so")
     assert build.build_fastcall() not in (first, second) and len(made) == 3
+
+
+def test_library_is_built_without_torch_or_the_native_part(monkeypatch):
+    """The C library first, whatever becomes of the binding's part."""
+    code = ("import sys; sys.modules['torch'] = None\nfrom mixture_experts_ffn_16_b200 import build\n"
+            "build._newer = lambda out, deps: out == build.LIB\nprint(build.build())")
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(build.HERE))
+    assert out.returncode == 0 and out.stdout.strip() == build.LIB, out.stderr
+    order = []
+
+    def failing(*args):
+        order.append("native part")
+        raise subprocess.CalledProcessError(1, "g++")
+
+    monkeypatch.setattr(build, "build_library", lambda *args: order.append("library") or build.LIB)
+    monkeypatch.setattr(build, "build_fastcall", failing)
+    with pytest.warns(UserWarning, match="native part"):
+        assert build.build() == build.LIB
+    assert order == ["library", "native part"]
+
+
+@pytest.fixture
+def no_native_part(monkeypatch, tmp_path):
+    monkeypatch.setattr(build, "fastcall_path", lambda: str(tmp_path / "_fastcall.so"))
+    monkeypatch.setattr(api, "_fastcall", None)
+    with pytest.warns(UserWarning, match="ctypes"):
+        api._fast()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_without_the_native_part_the_python_part_checks(name, no_native_part):
+    args, outs = arguments(name, "cpu")
+    assert native(name, args) is None
+    with pytest.raises(ValueError):                      # tensors of the host
+        getattr(api, "moe_" + name)(*args)
+    assert all(not o.any() for o in outs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_without_the_native_part_the_python_part_makes_the_calls(name, no_native_part):
+    want, want_outs = arguments(name, "cuda")
+    getattr(api, "moe_" + name)(*want, stream=torch.cuda.current_stream())
+    args, outs = arguments(name, "cuda")
+    getattr(api, "moe_" + name)(*args)
+    torch.cuda.synchronize()
+    assert any(o.any() for o in outs)
+    assert all(torch.equal(a, b) for a, b in zip(want_outs, outs))
