@@ -709,3 +709,34 @@ def test_scales_of_the_run_are_the_ones_used(N, K):
             api.moe_swiglu_fp4(a, off, w, up, h, ws)
             assert all(torch.equal(p, q) for p, q in zip(first, (out, *h)))
     assert api.moe_device_status(ws) == api.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [130, 700])             # single CTAs, CTA pairs
+@pytest.mark.parametrize("off", [[0, 90, 40, 200], [-7, 3, 10 ** 9, 5], [200, 100, 50, 0], [300, 300, 300, 300],
+                                 [0, 699, 1, 2 ** 31 - 1], [-2 ** 31, 650, -1, 700]])
+def test_invalid_offsets_stay_in_bounds_in_every_form(off, rows, dtype):
+    """Of both products: what lies around their outputs stays as it was."""
+    rng = np.random.default_rng(5)
+    N, K, pad = 192, 320, 64
+    a, _ = random_fp4(rng, 1, rows, K)
+    w, _ = random_fp4(rng, 3, N, K)
+    offsets, ws = dev(np.array(off, dtype=np.int32)), api.alloc_dispatch_workspace()
+
+    def guarded(shape, dtype):
+        """A tensor of this shape with `pad` rows' worth of other bytes on either side, and those bytes."""
+        n, around = int(np.prod(shape)), pad * N
+        room = torch.full((n + 2 * around,), 93, dtype=dtype, device="cuda")
+        return room[around:around + n].view(shape), lambda: bool((room[:around] == 93).all() and
+                                                                 (room[around + n:] == 93).all())
+
+    out, out_kept = guarded((rows, N), dtype)
+    codes, codes_kept = guarded((1, rows, N // 2), torch.uint8)
+    scales, scales_kept = guarded((1, 2, rows, 4), torch.uint8)
+    api.moe_matmul_fp4(a, offsets, w, out, ws)
+    api.moe_swiglu_fp4(a, offsets, w, w, (codes, scales), ws)
+    assert api.moe_device_status(ws) == api.MOE_OK
+    assert out_kept() and codes_kept() and scales_kept()
+    low, high = np.clip([min(off), max(off)], 0, rows)
+    for t in (out, codes[0], scales[0].transpose(0, 1).reshape(rows, -1)):       # rows that no offsets enclose
+        assert bool((t[:low] == 93).all() and (t[high:] == 93).all())
