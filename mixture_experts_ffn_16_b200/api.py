@@ -248,6 +248,8 @@ def _p(t, dtype=None, shape=None, name="", host=False):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
+    if t.is_neg():                   # the memory holds the negated values
+        raise ValueError(f"{name}: a view that negates another tensor (take its resolve_neg())")
     return ctypes.c_void_p(t.data_ptr())
 
 
@@ -536,7 +538,7 @@ def _dev(t):
 def _t(t, dtype, shape, name, dev):
     """Address of a contiguous tensor of this type and shape (None: any) on device `dev`."""
     if (type(t) is torch.Tensor and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()
-            and t.get_device() == dev >= 0):
+            and not t.is_neg() and t.get_device() == dev >= 0):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
@@ -565,7 +567,7 @@ def _f4(q, G, rows, K, name, dev):
     u8 = torch.uint8
     if (type(s) is torch.Tensor and c.dtype is u8 and s.dtype is u8 and c.shape == (G, rows, K // 2)
             and s.shape == (G, (K + 127) // 128, rows, 4) and c.is_contiguous() and s.is_contiguous()
-            and c.get_device() == s.get_device() == dev >= 0):
+            and not (c.is_neg() or s.is_neg()) and c.get_device() == s.get_device() == dev >= 0):
         return MoeFp4Tensor(c.data_ptr(), s.data_ptr())
     return MoeFp4Tensor(_t(c, u8, (G, rows, K // 2), name + ".codes", dev),
                         _t(s, u8, (G, (K + 127) // 128, rows, 4), name + ".scales", dev))

@@ -223,3 +223,27 @@ def test_without_the_native_part_the_python_part_makes_the_calls(name, no_native
     torch.cuda.synchronize()
     assert any(o.any() for o in outs)
     assert all(torch.equal(a, b) for a, b in zip(want_outs, outs))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_refuses_views_that_negate(name):
+    """A lazily negated view is contiguous and has the right type, but its memory holds the other sign."""
+    args, outs = arguments(name, "cuda")
+    for i, a in enumerate(args):
+        for j in range(len(a) if isinstance(a, tuple) else 1):
+            bad = list(args)
+            if isinstance(a, tuple):
+                bad[i] = tuple(torch._neg_view(t) if q == j else t for q, t in enumerate(a))
+            else:
+                bad[i] = torch._neg_view(a)
+            assert native(name, bad) is None
+            with pytest.raises(ValueError, match="negates"):
+                getattr(api, "moe_" + name)(*bad)
+    torch.cuda.synchronize()
+    assert all(not o.any() for o in outs)
+
+
+def test_refuses_a_host_view_that_negates():
+    with pytest.raises(ValueError, match="x: .*negates"):
+        api._p(torch._neg_view(torch.ones(4, 8)), torch.float32, (4, 8), "x", host=True)
