@@ -740,3 +740,47 @@ def test_invalid_offsets_stay_in_bounds_in_every_form(off, rows, dtype):
     low, high = np.clip([min(off), max(off)], 0, rows)
     for t in (out, codes[0], scales[0].transpose(0, 1).reshape(rows, -1)):       # rows that no offsets enclose
         assert bool((t[:low] == 93).all() and (t[high:] == 93).all())
+
+
+def test_two_graphs_of_one_workspace_and_two_threads_at_once():
+    """Chains captured with the same dispatch workspace, replayed in turn; then two threads calling on streams of their
+    own, each with its workspace: the bits of the calls made alone."""
+    import threading
+    chains = [Chain(300, 256, 192, 5, 2, seed=31), Chain(64, 512, 128, 24, 6, seed=32)]
+    chains[1].ws = chains[0].ws
+    want = []
+    for c in chains:
+        c()
+        want.append(c.state())
+    torch.cuda.synchronize()
+    graphs = []
+    for c in chains:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c()
+    for _ in range(5):
+        for c, g, w in zip(chains, graphs, want):
+            for t in (c.idx, c.offsets, c.slot_row, *c.a, *c.h, c.y, c.out):
+                t.fill_(1)
+            g.replay()
+            assert all(torch.equal(p, q) for p, q in zip(w, c.state()))
+    chains[1].ws = api.alloc_dispatch_workspace()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(c, w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    c()
+                    if not all(torch.equal(p, q) for p, q in zip(w, c.state())):
+                        failed.append("differs")
+        except Exception as e:               # a thread's exception would be lost
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=p) for p in zip(chains, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and all(api.moe_device_status(c.ws) == api.MOE_OK for c in chains)
