@@ -31,16 +31,17 @@
 //               shared memory to 8 features of a token a lane.  16 warps were
 //               slower (product 284 -> 315 us at 384 experts of 165 rows).
 //
-// What bounds them, on a B200 under its 1 kW limit (random operands; a plain
-// copy of random data draws 0.88-0.97 kW there, 148 pJ a byte of HBM traffic):
-// experts of few rows stream their weights at the copy bandwidth (512 experts,
-// 640 rows, N = 4096, K = 1024: 115 us, 7.0 TB/s).  With many rows the power
-// limit binds: 64 experts x about 512 rows, N = K = 4096 takes 340 us (3.2
-// PFLOP/s, 1.4 GHz).  The MMAs alone, on operands that are already there, take
-// 175 us of the 1 kW, the tensor loads alone 184 us, loads and epilogue 245 us;
-// without the scales' copies to shared memory it takes 331 us, without those to
-// tensor memory 323 us.  The clock takes what is saved, up to 1.9 GHz.  DRAM
-// reads are the operands once (166 MB of 160 at 16 experts x 512 rows).
+// What bounds them, on a B200 under its 1 kW limit: experts of few rows stream
+// their weights (512 experts, 640 rows, N = 4096, K = 1024: 115 us on the same
+// tensors again, 124-127 us on others each time, 7.1 and 6.5-6.6 TB/s; a pass
+// that only reads 4 GiB reaches 7.26, a copy 6.56).  With many rows the power
+// limit binds: 64 experts x about 512 rows, N = K = 4096, takes 286 us from a
+// cool start and 333 us in a loop of seconds (3.3 PFLOP/s, 992 W, 1327 MHz).  Of
+// its 340 us at an earlier step the MMAs alone, on operands that are already
+// there, took 175, the tensor loads alone 184, loads and epilogue 245, all but
+// the scales' copies to shared memory 331, all but those to tensor memory 323;
+// the clock took what was saved, up to 1.9 GHz.  DRAM reads are the operands once
+// (164 MB of 160 at 16 experts x 512 rows).
 //
 // K need not be a multiple of 256: loads past its end read zeros, and the MMAs
 // past it are not issued.
@@ -226,7 +227,8 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, const
 
 // Every lane waits, since each goes on to touch what the barrier guards (a
 // shuffle from one that waits would not order the others' accesses); all or
-// none go on.
+// none go on.  Also faster than one lane and a shuffle: 64 experts x about 512
+// rows 346 -> 315 us.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const Params& p) {
   return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, p));
 }
@@ -272,9 +274,9 @@ __device__ __forceinline__ void xch_get8(const float* x, int tok, int feat, floa
 }
 
 // h of token `tok` of the run and features feat0 + 8 (lane & 3) .. + 7 as
-// MXFP4: the block's four lanes are neighbours.  (With a lane a feature and
-// the block's maximum by shuffles over 32 lanes, gate/up of 256 experts x 128
-// rows took 75 us.)
+// MXFP4: the block's four lanes are neighbours.  (Gate/up of 256 experts x 128
+// rows 76.0 us; with a lane a feature and the block's maximum by shuffles over
+// 32 lanes 77.6 us.)
 __device__ __forceinline__ void emit_h8(const Params& p, const Unit& un, int feat0, int tok, const float (&h)[8],
                                         int lane) {
   uint32_t m = 0;
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_gemm_kernel(const __grid_cons
 // Against runs of up to 192 in two fixed places, 32 experts of 160 / 256 / 320
 // / 512 / 2048 rows, N = 2048, K = 4096: 36.7 / 55.9 / 61.7 / 93.0 / 311 us
 // there, 36.4 / 46.9 / 62.2 / 84.0 / 285 us this way (without the early report
-// longer runs gained nothing at 512 rows).
+// longer runs gained nothing at 512 rows; all of it at an earlier step).
 //   product: CTA r has output features 128 r .. of the unit's 256.
 //   swiglu:  CTA r has features 64 r .. of the unit's 128, their gate rows in
 //            lanes 0..63 and their up rows in lanes 64..127.  A gate warp and
@@ -986,11 +988,11 @@ int launch_kind(const Params& prm, bool pair, int sms, cudaStream_t st) {
 int launch_fp4_product(const Fp4Product& q, const DeviceInfo& di, uint32_t* err, cudaStream_t st) {
   const bool swiglu = q.w1_codes != nullptr;
   // CTA pairs above 96 rows an expert on average, what a single CTA's unit
-  // takes in one run.  64 experts of 96 / 104 / 128 / 512 rows, pairs against
-  // single CTAs: N = 4096, K = 1024 product 39 / 39 / 42 / 121 us against 34 /
-  // 44 / 46 / 146; f = 1024, K = 4096 gate/up 59 / 61 / 64 / 170 against 55 /
-  // 66 / 68 / 211.  256 experts of 96 rows on average, the largest 48 times the
-  // smallest: gate/up 259 against 244.
+  // takes in one run.  64 experts of 80 / 96 / 104 / 128 / 512 rows, pairs
+  // against single CTAs: N = 4096, K = 1024 product 33 / 35 / 35 / 40 / 114 us
+  // against 28 / 30 / 43 / 46 / 149; f = 1024, K = 4096 gate/up 55 / 59 / 57 / 62 /
+  // 174 against 51 / 55 / 63 / 72 / 219.  256 experts of 96 rows on average, the
+  // largest 48 times the smallest: gate/up 266 against 245.
   const int64_t avg = (static_cast<int64_t>(q.rows) + q.E - 1) / q.E;
   const bool pair = avg > Single::NMAX && di.sms >= 2;
   Params p;
