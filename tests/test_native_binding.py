@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import fp4_ref as ref
-from mixture_experts_ffn_16_b200 import api, build
+from mixture_experts_ffn_16_b200 import api
+from mixture_experts_ffn_16_b200 import build
 
 T, K, E, D, F = 37, 3, 5, 192, 128
 NAMES = ["sort_tokens", "dispatch", "dispatch_backward", "undispatch", "undispatch_backward", "quantize_fp4",
